@@ -7,7 +7,8 @@ and passes raw device pointers plus the current stream. There is no CPU fallback
 the library is missing, every call raises.
 
 Functions mirror the C entry points of ``include/binattn.h``:
-``pack_signs``, ``quant_v``, ``attention_fwd``, ``attention_fwd_packed``.
+``pack_signs``, ``quant_v``, ``attention_fwd``, ``attention_fwd_packed``, and for sequences
+that grow ``KVCache`` with ``cache_write``, ``cache_read`` and ``attention_paged``.
 """
 from __future__ import annotations
 
@@ -43,6 +44,19 @@ class CBias(ctypes.Structure):
                 ("table_w", ctypes.c_int), ("n_prefix", ctypes.c_int)]
 
 
+class CKvCache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int),
+                ("n_kv_heads", ctypes.c_int), ("d", ctypes.c_int)]
+
+
+class CPagedSeqs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int64), ("n_heads", ctypes.c_int),
+                ("max_q_len", ctypes.c_int), ("max_kv_len", ctypes.c_int64), ("cu_seqlens_q", ctypes.c_void_p),
+                ("kv_lens", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("max_pages", ctypes.c_int), ("causal", ctypes.c_int), ("window", ctypes.c_int),
+                ("sinks", ctypes.c_int)]
+
+
 _lib = None
 
 _P, _I, _F, _SZ, _I64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64
@@ -65,6 +79,12 @@ SIGNATURES = {
                                     _P, _P, _I, _P]),
     "ba_attention_fwd_noalloc": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, ctypes.POINTER(CBias), _F, _P, _I, _P,
                                       _P]),
+    "ba_kv_block_bytes": (_SZ, [_I, _I]),
+    "ba_cache_write": (_I, [_P, _I64, _I64, _P, _I64, _I64, _I, _I64, _P, ctypes.POINTER(CKvCache), _P]),
+    "ba_cache_read": (_I, [ctypes.POINTER(CKvCache), _P, _I64, _P, _P, _I, _P]),
+    "ba_paged_workspace_bytes": (_SZ, [ctypes.POINTER(CKvCache), ctypes.POINTER(CPagedSeqs)]),
+    "ba_attention_paged": (_I, [_P, _I64, _I64, _I, ctypes.POINTER(CKvCache), ctypes.POINTER(CPagedSeqs), _F, _P,
+                                _I, _P, _P, _SZ, _P]),
     "ba_set_attention_impl": (_I, [_I]),
     "ba_get_attention_impl": (_I, []),
     "ba_last_attention_impl": (_I, []),
@@ -302,6 +322,217 @@ def attention_fwd_debug(q, k, v, bias: Optional[Bias] = None, softmax_scale: flo
                                         workspace.numel(), _ptr(dbg), _ptr(dbg_p), 1 if check_all_codes else 0,
                                         _stream(stream)), "ba_attention_fwd_debug")
     return out, dbg, dbg_p
+
+
+# ----------------------------------------------------------------------------- paged cache
+def kv_block_bytes(page_size: int, d: int) -> int:
+    """Bytes of the cache rows of one page of one KV head (0 for unsupported sizes)."""
+    return lib().ba_kv_block_bytes(page_size, d)
+
+
+@dataclass
+class KVCache:
+    """A paged cache of binary K and 8-bit V rows (layout: include/binattn.h, ba_kv_cache).
+
+    data: uint8 CUDA tensor [num_pages, n_kv_heads, kv_block_bytes(page_size, d)], contiguous.
+    ``KVCache.zeros`` allocates one; any slice of a larger buffer of that shape does as well.
+    """
+    data: object
+    page_size: int
+    d: int
+
+    @classmethod
+    def zeros(cls, num_pages: int, n_kv_heads: int, d: int, page_size: int = 64, device="cuda") -> "KVCache":
+        nbytes = kv_block_bytes(page_size, d)
+        if nbytes == 0:
+            raise ValueError("page_size must be a multiple of 16 up to 1024, d between 1 and 128")
+        torch = _torch()
+        return cls(torch.zeros((num_pages, n_kv_heads, nbytes), dtype=torch.uint8, device=device), page_size, d)
+
+    @property
+    def num_pages(self) -> int:
+        return self.data.shape[0]
+
+    @property
+    def n_kv_heads(self) -> int:
+        return self.data.shape[1]
+
+    def _part(self, at: int, width: int):
+        return self.data[:, :, self.page_size * at:self.page_size * (at + width)]
+
+    @property
+    def v_codes(self):
+        """int8 codes of V [num_pages, n_kv_heads, page_size, v_row_bytes(d)] (a view)."""
+        dp = v_row_bytes(self.d)
+        return self._part(0, dp).view(_torch().int8).unflatten(2, (self.page_size, dp))
+
+    @property
+    def k_bits(self):
+        """Sign words of K, int32 [num_pages, n_kv_heads, page_size, 4] (a view)."""
+        return self._part(v_row_bytes(self.d), 16).view(_torch().int32).unflatten(2, (self.page_size, 4))
+
+    @property
+    def k_mu(self):
+        """bf16 scales of K [num_pages, n_kv_heads, page_size] (a view)."""
+        return self._part(v_row_bytes(self.d) + 16, 2).view(_torch().bfloat16)
+
+    @property
+    def v_exp(self):
+        """int8 exponents of V [num_pages, n_kv_heads, page_size] (a view)."""
+        return self._part(v_row_bytes(self.d) + 18, 1).view(_torch().int8)
+
+    def c(self) -> CKvCache:
+        torch = _torch()
+        t = self.data
+        if t.dtype != torch.uint8 or t.dim() != 3 or not t.is_cuda or not t.is_contiguous():
+            raise ValueError("cache data must be a contiguous uint8 CUDA tensor [pages, heads, block bytes]")
+        if t.shape[2] != kv_block_bytes(self.page_size, self.d) or t.shape[2] == 0:
+            raise ValueError("cache blocks must have kv_block_bytes(page_size, d) bytes")
+        return CKvCache(t.data_ptr(), t.shape[0], self.page_size, t.shape[1], self.d)
+
+
+class _On:
+    """Makes a tensor's device current, and a given stream too, so that what torch allocates inside
+    belongs to the stream the kernels run on; `stream` is then that stream's handle."""
+
+    def __init__(self, t, stream):
+        torch = _torch()
+        self.ctx = None
+        if stream is not None:
+            if stream.device != t.device:
+                raise ValueError("stream and tensors must be on one device")
+            self.ctx = torch.cuda.stream(stream)
+        elif t.device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(t.device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return _stream()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _same_device(ref, **ts):
+    for name, t in ts.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} must be on the cache's device")
+
+
+def _index_check(t, name: str, dtype, shape=None):
+    if t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}")
+
+
+def _rows_check(t, name: str, heads, d: int):
+    torch = _torch()
+    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens, heads, {d}] with the cache's heads")
+    if t.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"{name} must be fp16 or bf16")
+    if t.stride(2) != 1 and d > 1 and t.numel() > 0:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+def cache_write(cache: KVCache, k, v, slots, stream=None) -> None:
+    """Quantise new rows k, v [T, n_kv_heads, d] (fp16/bf16; strided views are taken as they are)
+    and write them to the tokens at slots (int64 [T], page * page_size + offset; -1 skips a row).
+    Slots in range must differ."""
+    cc = cache.c()
+    _rows_check(k, "k", cc.n_kv_heads, cache.d)
+    _rows_check(v, "v", cc.n_kv_heads, cache.d)
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must share dtype and shape")
+    _same_device(cache.data, k=k, v=v, slots=slots)
+    _index_check(slots, "slots", _torch().int64, (k.shape[0],))
+    with _On(cache.data, stream) as s:
+        _check(lib().ba_cache_write(_ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1), _dt(k),
+                                    k.shape[0], _ptr(slots), ctypes.byref(cc), s), "ba_cache_write")
+
+
+def cache_read(cache: KVCache, slots, dtype=None, k_out=None, v_out=None, stream=None) -> Tuple[object, object]:
+    """(k, v) [T, n_kv_heads, d]: the rows at slots (int64 [T]) as numbers; rows out of range are 0.
+    dtype: fp16, bf16 (default) or fp32, or that of k_out / v_out where they are given."""
+    torch = _torch()
+    cc = cache.c()
+    _same_device(cache.data, slots=slots, k_out=k_out, v_out=v_out)
+    _index_check(slots, "slots", torch.int64, (slots.numel(),))
+    shape = (slots.numel(), cc.n_kv_heads, cache.d)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is not None:
+            dtype = dtype or t.dtype
+            _index_check(t, name, dtype, shape)
+    dtype = dtype or torch.bfloat16
+    with _On(cache.data, stream) as s:
+        k = torch.empty(shape, dtype=dtype, device=slots.device) if k_out is None else k_out
+        v = torch.empty(shape, dtype=dtype, device=slots.device) if v_out is None else v_out
+        _check(lib().ba_cache_read(ctypes.byref(cc), _ptr(slots), shape[0], _ptr(k), _ptr(v), _dt(k), s),
+               "ba_cache_read")
+    return k, v
+
+
+def _paged_seqs(q, cc, page_size, page_table, kv_lens, cu_seqlens_q, max_q_len, max_kv_len, causal, window, sinks):
+    torch = _torch()
+    B = kv_lens.numel()
+    _index_check(kv_lens, "kv_lens", torch.int32, (B,))
+    if cu_seqlens_q is not None:
+        _index_check(cu_seqlens_q, "cu_seqlens_q", torch.int32, (B + 1,))
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B or \
+            (page_table.stride(1) != 1 and page_table.shape[1] > 1):
+        raise ValueError("page_table must be an int32 tensor [sequences, pages], contiguous in its last dimension")
+    pages = page_table.shape[1]
+    if max_q_len is None:
+        max_q_len = 1 if cu_seqlens_q is None else q.shape[0]
+    if max_kv_len is None:
+        max_kv_len = pages * page_size
+    return CPagedSeqs(B, q.shape[0], q.shape[1], max_q_len, max_kv_len,
+                      0 if cu_seqlens_q is None else cu_seqlens_q.data_ptr(), kv_lens.data_ptr(),
+                      page_table.data_ptr(), page_table.stride(0), pages, 1 if causal else 0, window, sinks)
+
+
+def attention_paged(q, cache: KVCache, page_table, kv_lens, cu_seqlens_q=None, max_q_len: Optional[int] = None,
+                    max_kv_len: Optional[int] = None, causal: bool = True, window: int = 0, sinks: int = 0,
+                    softmax_scale: float = 0.0, out=None, out_dtype=None, return_lse: bool = False, workspace=None,
+                    stream=None):
+    """Attention of new tokens over the cache, which holds their own rows too (ba_attention_paged).
+
+    q:            [T, n_heads, d] fp16/bf16, a strided view at will; the new tokens of all sequences.
+    page_table:   int32 [B, pages]: page of each page_size tokens of a sequence.
+    kv_lens:      int32 [B]: tokens in the cache, the new ones included.
+    cu_seqlens_q: int32 [B + 1]: sequence b has rows cu[b] .. cu[b + 1] - 1; None: one row each.
+    max_q_len, max_kv_len: host bounds of the lengths (defaults: T, and the page table's tokens).
+                  Tight bounds let the launch be chosen well; lengths are read on the device.
+    window:       > 0: a token sees itself and the window - 1 tokens before it, and the first `sinks`.
+    Returns o [T, n_heads, d] (out_dtype, default q's; rows of no sequence are left as they were in
+    `out`), and with return_lse also the fp32 log of the softmax sums [T, n_heads].
+    """
+    torch = _torch()
+    cc = cache.c()
+    _rows_check(q, "q", None, cache.d)
+    _same_device(cache.data, q=q, page_table=page_table, kv_lens=kv_lens, cu_seqlens_q=cu_seqlens_q, out=out,
+                 workspace=workspace)
+    sq = _paged_seqs(q, cc, cache.page_size, page_table, kv_lens, cu_seqlens_q, max_q_len, max_kv_len, causal,
+                     window, sinks)
+    if out is not None:
+        _index_check(out, "out", out_dtype or out.dtype, tuple(q.shape))
+    with _On(cache.data, stream) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
+        nws = lib().ba_paged_workspace_bytes(ctypes.byref(cc), ctypes.byref(sq))
+        if nws == ctypes.c_size_t(-1).value:  # unsupported: the call below reports it
+            nws = 0
+        if workspace is None:
+            workspace = torch.empty(nws, dtype=torch.uint8, device=q.device) if nws else None
+        _check(lib().ba_attention_paged(_ptr(q), q.stride(0), q.stride(1), _dt(q), ctypes.byref(cc),
+                                        ctypes.byref(sq), float(softmax_scale), _ptr(out), _dt(out), _ptr(lse),
+                                        _ptr(workspace), 0 if workspace is None else workspace.numel(), s),
+               "ba_attention_paged")
+    return (out, lse) if return_lse else out
 
 
 def bias_from_workload(w, device) -> Optional[Bias]:

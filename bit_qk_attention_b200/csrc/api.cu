@@ -218,6 +218,10 @@ ba_status run_attention(const AttnParams& ap, cudaStream_t s) {
 
 }  // namespace
 
+namespace binattn {
+ba_status report_cuda(cudaError_t e) { return cuda_status(e); }
+}  // namespace binattn
+
 extern "C" {
 
 int ba_sign_words(int d) { return (d >= 1 && d <= 128) ? kSignWords : 0; }

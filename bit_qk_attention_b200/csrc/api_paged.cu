@@ -1,0 +1,182 @@
+// C-ABI layer of the paged cache: argument checks and launches. The entry points are declared and
+// documented in include/binattn.h.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "binattn.h"
+#include "kernels.h"
+#include "paged.cuh"
+
+using namespace binattn;
+
+namespace {
+
+constexpr int64_t kMaxRows = int64_t{1} << 31;  // (token, head) rows of a call
+constexpr int64_t kMaxKv = int64_t{1} << 28;
+constexpr int64_t kMaxCtas = (int64_t{1} << 31) - 1;
+
+bool aligned(const void* p, unsigned n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+ba_status check_cache(const ba_kv_cache* c, CacheView* out) {
+  if (c == nullptr || c->num_pages < 0 || c->n_kv_heads < 0) return BA_ERR_INVALID_ARG;
+  if (ba_kv_block_bytes(c->page_size, c->d) == 0 || c->n_kv_heads < 1 || c->n_kv_heads > 65535)
+    return BA_ERR_UNSUPPORTED;
+  if (c->num_pages > (int64_t{1} << 40) / c->page_size) return BA_ERR_UNSUPPORTED;
+  if (c->num_pages > 0 && c->data == nullptr) return BA_ERR_INVALID_ARG;
+  if (!aligned(c->data, 16)) return BA_ERR_ALIGNMENT;
+  out->data = static_cast<uint8_t*>(c->data);
+  out->num_pages = c->num_pages;
+  out->page_size = c->page_size;
+  out->heads = c->n_kv_heads;
+  out->d = c->d;
+  out->dp = v_row_bytes(c->d);
+  out->block_bytes = static_cast<int64_t>(ba_kv_block_bytes(c->page_size, c->d));
+  return BA_OK;
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();  // no device here: the workspace query still answers
+    return 148;
+  }
+  return sms;
+}
+
+size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// Everything of a call that does not depend on its tensors: sizes, the kernel's tiles and splits,
+// and the workspace.
+ba_status plan(const ba_kv_cache* cache, const ba_paged_seqs* s, PagedAttnParams* p, size_t* ws) {
+  *ws = 0;
+  ba_status st = check_cache(cache, &p->cache);
+  if (st != BA_OK) return st;
+  if (s == nullptr || s->B < 0 || s->T < 0 || s->n_heads < 1 || s->max_q_len < 0 || s->max_kv_len < 0 ||
+      s->max_pages < 0 || s->table_stride < 0 || s->window < 0 || s->sinks < 0)
+    return BA_ERR_INVALID_ARG;
+  if (s->causal != 0 && s->causal != 1) return BA_ERR_INVALID_ARG;
+  if (s->window > 0 && s->causal != 1) return BA_ERR_INVALID_ARG;
+  if (s->n_heads % cache->n_kv_heads != 0) return BA_ERR_INVALID_ARG;
+  if (s->max_kv_len > kMaxKv || s->T > kMaxRows / s->n_heads) return BA_ERR_UNSUPPORTED;
+  p->B = s->B;
+  p->heads = s->n_heads;
+  p->group = s->n_heads / cache->n_kv_heads;
+  p->T = s->T;
+  p->max_q_len = static_cast<int>(std::min<int64_t>(s->cu_seqlens_q != nullptr ? s->max_q_len : std::min(s->max_q_len, 1), s->T));
+  p->max_kv_len = static_cast<int>(std::min<int64_t>(s->max_kv_len, static_cast<int64_t>(s->max_pages) * cache->page_size));
+  p->cu = s->cu_seqlens_q;
+  p->kv_lens = s->kv_lens;
+  p->table = s->page_table;
+  p->table_stride = s->table_stride;
+  p->causal = s->causal;
+  p->window = s->window;
+  p->sinks = s->sinks;
+  if (p->B == 0 || p->max_q_len == 0) return BA_OK;  // nothing to launch
+  const int64_t rows = static_cast<int64_t>(p->max_q_len) * p->group;
+  p->row_tile = rows <= 8 ? 8 : 16;
+  const int64_t tiles = ceil_div(rows, p->row_tile);
+  if (tiles > kMaxCtas / (static_cast<int64_t>(p->B) * p->cache.heads)) return BA_ERR_UNSUPPORTED;
+  p->row_tiles = static_cast<int>(tiles);
+  p->nsplit = paged_decode_splits(*p, sm_count());
+  if (tiles * p->B * p->cache.heads > kMaxCtas / std::max(p->nsplit, 4)) return BA_ERR_UNSUPPORTED;
+  if (p->nsplit > 1) {
+    const size_t n = static_cast<size_t>(p->nsplit) * p->T * p->heads;
+    *ws = align_up(n * p->cache.dp * 4) + align_up(n * 8);
+  }
+  return BA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ba_kv_block_bytes(int page_size, int d) {
+  if (d < 1 || d > 128 || page_size < kPageUnit || page_size > kMaxPage || page_size % kPageUnit != 0) return 0;
+  return static_cast<size_t>(page_size) * (v_row_bytes(d) + 19);
+}
+
+ba_status ba_cache_write(const void* k, int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                         int64_t v_stride_h, ba_dtype dt, int64_t T, const int64_t* slots, const ba_kv_cache* cache,
+                         void* stream) {
+  CacheWriteParams p{};
+  const ba_status st = check_cache(cache, &p.cache);
+  if (st != BA_OK) return st;
+  if (dt != BA_F16 && dt != BA_BF16) return BA_ERR_INVALID_ARG;
+  if (T < 0 || k_stride_t < 0 || k_stride_h < 0 || v_stride_t < 0 || v_stride_h < 0) return BA_ERR_INVALID_ARG;
+  if (T > kMaxRows / cache->n_kv_heads) return BA_ERR_UNSUPPORTED;
+  if (T == 0 || cache->num_pages == 0) return BA_OK;
+  if (!k || !v || !slots) return BA_ERR_INVALID_ARG;
+  if (!aligned(k, 2) || !aligned(v, 2) || !aligned(slots, 8)) return BA_ERR_ALIGNMENT;
+  p.k = k;
+  p.v = v;
+  p.k_stride_t = k_stride_t;
+  p.k_stride_h = k_stride_h;
+  p.v_stride_t = v_stride_t;
+  p.v_stride_h = v_stride_h;
+  p.T = T;
+  p.slots = slots;
+  p.wide = cache->d % 8 == 0 && aligned(k, 16) && aligned(v, 16) &&
+           (k_stride_t | k_stride_h | v_stride_t | v_stride_h) % 8 == 0;
+  return report_cuda(launch_cache_write(p, dt, static_cast<cudaStream_t>(stream)));
+}
+
+ba_status ba_cache_read(const ba_kv_cache* cache, const int64_t* slots, int64_t T, void* k, void* v, ba_dtype dt,
+                        void* stream) {
+  CacheReadParams p{};
+  const ba_status st = check_cache(cache, &p.cache);
+  if (st != BA_OK) return st;
+  if (dt != BA_F16 && dt != BA_BF16 && dt != BA_F32) return BA_ERR_INVALID_ARG;
+  if (T < 0) return BA_ERR_INVALID_ARG;
+  if (T > kMaxRows / cache->n_kv_heads) return BA_ERR_UNSUPPORTED;
+  if (T == 0 || (!k && !v)) return BA_OK;
+  if (!slots) return BA_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8)) return BA_ERR_ALIGNMENT;
+  p.slots = slots;
+  p.T = T;
+  p.k = k;
+  p.v = v;
+  return report_cuda(launch_cache_read(p, dt, static_cast<cudaStream_t>(stream)));
+}
+
+size_t ba_paged_workspace_bytes(const ba_kv_cache* cache, const ba_paged_seqs* seqs) {
+  PagedAttnParams p{};
+  size_t ws = 0;
+  return plan(cache, seqs, &p, &ws) == BA_OK ? ws : static_cast<size_t>(-1);
+}
+
+ba_status ba_attention_paged(const void* q, int64_t q_stride_t, int64_t q_stride_h, ba_dtype dt,
+                             const ba_kv_cache* cache, const ba_paged_seqs* seqs, float softmax_scale, void* o,
+                             ba_dtype o_dt, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  PagedAttnParams p{};
+  size_t need = 0;
+  const ba_status st = plan(cache, seqs, &p, &need);
+  if (st != BA_OK) return st;
+  if (dt != BA_F16 && dt != BA_BF16) return BA_ERR_INVALID_ARG;
+  if (o_dt != BA_F16 && o_dt != BA_BF16 && o_dt != BA_F32) return BA_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale) || q_stride_t < 0 || q_stride_h < 0) return BA_ERR_INVALID_ARG;
+  if (p.B == 0 || p.max_q_len == 0) return BA_OK;
+  if (!q || !o || !p.kv_lens || (p.max_kv_len > 0 && !p.table)) return BA_ERR_INVALID_ARG;
+  if (!aligned(q, 2) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(p.cu, 4) || !aligned(p.kv_lens, 4) ||
+      !aligned(p.table, 4))
+    return BA_ERR_ALIGNMENT;
+  if (need > 0) {
+    if (ws == nullptr || ws_bytes < need) return BA_ERR_WORKSPACE;
+    if (!aligned(ws, 16)) return BA_ERR_ALIGNMENT;
+    p.part_o = static_cast<float*>(ws);
+    const size_t n = static_cast<size_t>(p.nsplit) * p.T * p.heads;
+    p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + align_up(n * p.cache.dp * 4));
+  }
+  p.q = q;
+  p.q_stride_t = q_stride_t;
+  p.q_stride_h = q_stride_h;
+  const float scale = softmax_scale > 0.0f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(cache->d));
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.o = o;
+  p.o_dt = o_dt;
+  p.lse = lse;
+  return report_cuda(launch_paged_decode(p, dt, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

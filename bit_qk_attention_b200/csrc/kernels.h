@@ -84,6 +84,9 @@ bool attn_tc_supported(const AttnParams& p);
 double p_code_threshold(int k);  // the exact-code threshold table of the tcgen05 kernel
 cudaError_t launch_attn_tc(const AttnParams& p, cudaStream_t s);
 
+// BA_OK, or BA_ERR_CUDA with e kept for ba_last_cuda_error() on this thread.
+ba_status report_cuda(cudaError_t e);
+
 // Device status word of the kernels with bounded waits.
 cudaError_t read_and_clear_device_status(int* value, cudaStream_t s);
 

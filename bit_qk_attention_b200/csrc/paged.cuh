@@ -1,0 +1,118 @@
+// The paged KV cache as the kernels see it (the layout is documented in include/binattn.h).
+#pragma once
+
+#include "common.cuh"
+
+namespace binattn {
+
+constexpr int kMinExp = -24, kMaxExp = 9;  // exponents of a cached V row
+constexpr int kPageUnit = 16;              // a page holds a multiple of this many tokens
+constexpr int kMaxPage = 1024;
+
+struct CacheView {
+  uint8_t* data;
+  int64_t num_pages;
+  int page_size, heads, d, dp;
+  int64_t block_bytes;
+
+  // Offsets of the parts of a block.
+  __host__ __device__ int off_bits() const { return page_size * dp; }
+  __host__ __device__ int off_mu() const { return page_size * (dp + 16); }
+  __host__ __device__ int off_exp() const { return page_size * (dp + 18); }
+  __device__ uint8_t* block(int64_t page, int head) const { return data + (page * heads + head) * block_bytes; }
+};
+
+struct CacheWriteParams {
+  CacheView cache;
+  const void* k;
+  const void* v;
+  int64_t k_stride_t, k_stride_h, v_stride_t, v_stride_h;  // elements
+  int64_t T;
+  const int64_t* slots;
+  bool wide;  // every row of k and v starts on 16 bytes and d is a multiple of 8
+};
+
+struct CacheReadParams {
+  CacheView cache;
+  const int64_t* slots;
+  int64_t T;
+  void* k;
+  void* v;
+};
+
+// Attention of new tokens over the cache.
+struct PagedAttnParams {
+  CacheView cache;
+  const void* q;
+  int64_t q_stride_t, q_stride_h;  // elements
+  int B, heads, group;             // group = query heads per KV head
+  int64_t T;
+  int max_q_len, max_kv_len;  // max_kv_len also within the page table
+  const int32_t* cu;          // null: one row per sequence
+  const int32_t* kv_lens;
+  const int32_t* table;
+  int64_t table_stride;
+  int causal, window, sinks;
+  float scale_log2;  // softmax scale * log2(e)
+  void* o;
+  int o_dt;
+  float* lse;
+  int nsplit;      // parts of the key axis (most)
+  int row_tile;    // rows (token, head of the group) of a CTA's tile
+  int row_tiles;   // tiles of a sequence and KV head (most)
+  float* part_o;   // [nsplit][T * heads][dp] unnormalised sums, when nsplit > 1
+  float2* part_ml; // [nsplit][T * heads] (maximum in log2, sum)
+};
+
+// What a CTA works on: a tile of rows r = i * group + g (i-th new token, g-th head of the group) of
+// one sequence and KV head, against the keys that any of them sees. The keys are counted in blocks
+// of `bk` tokens: the blocks of the sinks, then those from the window's start to the last key.
+struct RowTile {
+  int64_t t0;     // row of q of the sequence's first new token
+  int nq, kv;     // new tokens, tokens in the cache
+  int r0, rows;   // first row of the tile, rows in it (<= 0: nothing to do)
+  int nsink, first, nblk;  // sink blocks, first block after them, blocks in all
+
+  __device__ int block_at(int v) const { return v < nsink ? v : first + (v - nsink); }
+  __device__ int pos0() const { return kv - nq; }  // position of the first new token
+};
+
+__device__ __forceinline__ RowTile row_tile(const PagedAttnParams& p, int b, int tile, int bk) {
+  RowTile w;
+  int64_t n;
+  if (p.cu != nullptr) {
+    w.t0 = min(max(static_cast<int64_t>(p.cu[b]), int64_t{0}), p.T);
+    n = min(max(static_cast<int64_t>(p.cu[b + 1]), w.t0), p.T) - w.t0;
+  } else {
+    w.t0 = b;
+    n = b < p.T ? 1 : 0;
+  }
+  w.nq = static_cast<int>(min(n, int64_t{1} << 28));
+  w.kv = min(max(p.kv_lens[b], 0), p.max_kv_len);
+  w.r0 = tile * p.row_tile;
+  w.rows = static_cast<int>(min(static_cast<int64_t>(p.row_tile),
+                                static_cast<int64_t>(min(w.nq, p.max_q_len)) * p.group - w.r0));
+  int lo = 0, hi = w.kv;
+  if (p.causal && w.rows > 0) {
+    hi = min(hi, w.pos0() + (w.r0 + w.rows - 1) / p.group + 1);
+    if (p.window > 0) lo = max(0, w.pos0() + w.r0 / p.group - p.window + 1);
+  }
+  w.first = lo / bk;
+  w.nsink = min(static_cast<int>(ceil_div(p.sinks, bk)), w.first);
+  w.nblk = hi <= 0 || w.rows <= 0 ? 0 : w.nsink + static_cast<int>(ceil_div(hi, bk)) - w.first;
+  return w;
+}
+
+// Splits that a tile of nblk blocks uses of the launch's nsplit: at least kMinSplit blocks each.
+__device__ __forceinline__ int splits_used(int nsplit, int nblk, int min_blocks) {
+  return max(1, min(nsplit, nblk / min_blocks));
+}
+
+cudaError_t launch_paged_decode(const PagedAttnParams& p, int dt, cudaStream_t s);
+// Parts of the key axis that the kernel is launched with on this device.
+int paged_decode_splits(const PagedAttnParams& p, int sms);
+
+cudaError_t launch_cache_write(const CacheWriteParams& p, int dt, cudaStream_t s);
+cudaError_t launch_cache_read(const CacheReadParams& p, int dt, cudaStream_t s);
+
+}  // namespace binattn

@@ -199,6 +199,118 @@ ba_status ba_attention_fwd_noalloc(const void* q, const void* k, const void* v, 
                                    ba_dtype o_dt, int32_t* dbg_logits, void* stream);
 
 /*
+ * ------------------------------------------------------------------ paged KV cache
+ * The binary attention of token sequences that grow: new K and V rows are quantised once, as
+ * they are written into a paged cache, and attention of new tokens reads them there.
+ *
+ * The scale of a key and of a value row cannot wait for the rows that follow, so both are per
+ * (token, head):
+ *   k^_c = mu * (1 - 2 bit_c),  bit_c = 1 iff k_c < 0 (as ba_pack_signs),
+ *          mu = mean_c |k_c| rounded to bf16;
+ *   v^_c = code_c * 2^e,  e = the least integer with max_c |v_c| <= 127 * 2^e, held to
+ *          [-24, 9], code_c = rne(v_c * 2^-e) held to [-127, 127]; a zero row has e = -24.
+ * mu in bf16 makes every k^_c a bf16 number, and the power of two makes every v^_c an fp16
+ * number (values beyond 127 * 2^9 = 65024 saturate there): the attention kernels feed both to
+ * the tensor cores without another rounding. A row takes dp + 19 bytes (dp = ba_v_row_bytes(d)):
+ * 147 at d = 128, where K and V in 16 bits take 512.
+ *
+ * Layout: data holds num_pages * n_kv_heads blocks [page][head] of ba_kv_block_bytes() bytes,
+ * each with the rows of page_size tokens:
+ *   int8   codes[page_size][dp]   (columns >= d are 0)
+ *   uint32 bits[page_size][4]     (bits >= d are 0)
+ *   bf16   mu[page_size]
+ *   int8   e[page_size]
+ * A token's slot is page * page_size + its offset in the page.
+ */
+typedef struct {
+  void* data;        /* device memory, aligned to 16 bytes */
+  int64_t num_pages; /* >= 0 */
+  int page_size;     /* tokens per page: a multiple of 16, 16 to 1024 */
+  int n_kv_heads;    /* 1 to 65535 */
+  int d;             /* 1 to 128 */
+} ba_kv_cache;
+
+/* Bytes of one (page, head) block: page_size * (dp + 19), a multiple of 16; 0 for sizes outside
+ * the limits above. */
+size_t ba_kv_block_bytes(int page_size, int d);
+
+/*
+ * Quantises T new tokens and writes them into the cache.
+ *   k, v:  row (t, h) starts at element t * stride_t + h * stride_h and has d contiguous elements
+ *          of dt (BA_F16 or BA_BF16): slices of a fused projection are taken as they are. These
+ *          two pointers need the alignment of their elements only (rows on 16-byte boundaries
+ *          with d a multiple of 8 are read with wide loads). Values must be finite (a row with
+ *          inf or NaN gets unspecified contents; other rows are not affected).
+ *   slots: [T] int64 (aligned to 8 bytes), the slot of each token. A slot outside
+ *          [0, num_pages * page_size) is skipped (padding: -1). A slot named twice in a call
+ *          ends with an unspecified mixture of its rows: slots in range have to differ.
+ */
+ba_status ba_cache_write(const void* k, int64_t k_stride_t, int64_t k_stride_h, const void* v,
+                         int64_t v_stride_t, int64_t v_stride_h, ba_dtype dt, int64_t T,
+                         const int64_t* slots, const ba_kv_cache* cache, void* stream);
+
+/*
+ * Reads T rows back: k[t][h][c] = k^, v[t][h][c] = v^ of the token in slots[t], contiguous
+ * [T][n_kv_heads][d] in dt (any ba_dtype; k^ is rounded to fp16 where dt is BA_F16, all else is
+ * exact). Rows whose slot is out of range are 0. k or v may be NULL (not wanted). A slot may be
+ * named any number of times.
+ */
+ba_status ba_cache_read(const ba_kv_cache* cache, const int64_t* slots, int64_t T, void* k, void* v,
+                        ba_dtype dt, void* stream);
+
+/*
+ * Attention of new tokens over the paged cache, for any mix of sequence lengths: one token each
+ * (decoding), a few (drafts), or a chunk of a prompt. The new tokens' own K and V rows are in the
+ * cache already (ba_cache_write), as the last ones of their sequence.
+ *
+ * Sequence b has the rows cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1 of q and o, n of them, and
+ * kv_lens[b] tokens in the cache, token j in page page_table[b][j / page_size]. Its i-th new token
+ * is at position p = kv_lens[b] - n + i and sees the tokens j < kv_lens[b] with
+ *   causal:      j <= p
+ *   window > 0:  j > p - window, or j < sinks  (the first tokens stay visible)
+ * Query heads g * G .. g * G + G - 1 use KV head g, G = n_heads / n_kv_heads.
+ *   s_j = softmax_scale * mu_q * mu_j * (d - 2 popc(sign bits of q XOR sign bits of k_j)),
+ *   mu_q = mean |q| of the row in fp32;  o = sum_j exp(s_j) v^_j / sum_j exp(s_j),
+ *   lse = log sum_j exp(s_j).
+ * There is no 8-bit P here: the weights are rounded to fp16 (relative 2^-11) for the product with
+ * V, which accumulates in fp32; scores, maxima and sums are fp32. A row that sees nothing gets
+ * o = 0 and lse = -inf.
+ */
+typedef struct {
+  int B;                       /* sequences */
+  int64_t T;                   /* rows of q and o; rows of no sequence are left as they were */
+  int n_heads;                 /* query heads, a multiple of the cache's n_kv_heads */
+  int max_q_len;               /* >= every sequence's new tokens; rows beyond are left as they were */
+  int64_t max_kv_len;          /* >= every kv_lens[b] (what is beyond it is not read); <= 2^28 */
+  const int32_t* cu_seqlens_q; /* [B + 1] ascending, or NULL: sequence b has the one row b */
+  const int32_t* kv_lens;      /* [B] */
+  const int32_t* page_table;   /* [B] rows of table_stride entries, the first max_pages of them valid;
+                                  a token whose page is outside [0, num_pages) is not seen */
+  int64_t table_stride;
+  int max_pages;
+  int causal;                  /* 0 or 1 */
+  int window;                  /* 0: none; > 0 wants causal = 1 */
+  int sinks;                   /* >= 0 */
+} ba_paged_seqs;
+
+/* Workspace of ba_attention_paged in bytes (partial sums of a split key axis; 0 when none is
+ * needed), or -1 cast to size_t for arguments that the call refuses. Reads no device memory. */
+size_t ba_paged_workspace_bytes(const ba_kv_cache* cache, const ba_paged_seqs* seqs);
+
+/*
+ *   q:   row (t, h) starts at element t * q_stride_t + h * q_stride_h, d contiguous elements of dt
+ *        (BA_F16 or BA_BF16), aligned to its elements; values must be finite.
+ *   o:   [T][n_heads][d] contiguous in o_dt (any ba_dtype).
+ *   lse: NULL, or [T][n_heads] fp32 out.
+ *   softmax_scale: <= 0 selects 1/sqrt(d).
+ *   The device arrays of seqs are aligned to 4 bytes. Lengths are read on the device, so a captured
+ *   call can be replayed with other lengths within max_q_len and max_kv_len.
+ */
+ba_status ba_attention_paged(const void* q, int64_t q_stride_t, int64_t q_stride_h, ba_dtype dt,
+                             const ba_kv_cache* cache, const ba_paged_seqs* seqs, float softmax_scale,
+                             void* o, ba_dtype o_dt, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Kernel choice for the fused step, process-wide: 0 = automatic (the tcgen05 tensor-core
  * kernel where it supports the shape, else the CUDA-core kernel), 1 = the CUDA-core kernel,
  * 2 = the tcgen05 kernel (BA_ERR_UNSUPPORTED for shapes it does not take).
