@@ -14,6 +14,8 @@ namespace {
 
 constexpr int64_t kMaxRows = int64_t{1} << 31;  // (token, head) rows of a call
 constexpr int64_t kMaxKv = int64_t{1} << 28;
+// Rows (new tokens x heads of a group) per sequence up to which the decoding kernel is taken.
+constexpr int kDecodeRows = 32;
 constexpr int64_t kMaxCtas = (int64_t{1} << 31) - 1;
 
 bool aligned(const void* p, unsigned n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -75,12 +77,12 @@ ba_status plan(const ba_kv_cache* cache, const ba_paged_seqs* s, PagedAttnParams
   p->sinks = s->sinks;
   if (p->B == 0 || p->max_q_len == 0) return BA_OK;  // nothing to launch
   const int64_t rows = static_cast<int64_t>(p->max_q_len) * p->group;
-  p->row_tile = rows <= 8 ? 8 : 16;
+  p->row_tile = rows <= 8 ? 8 : (rows <= kDecodeRows ? 16 : 256);
   const int64_t tiles = ceil_div(rows, p->row_tile);
   if (tiles > kMaxCtas / (static_cast<int64_t>(p->B) * p->cache.heads)) return BA_ERR_UNSUPPORTED;
   p->row_tiles = static_cast<int>(tiles);
-  p->nsplit = paged_decode_splits(*p, sm_count());
-  if (tiles * p->B * p->cache.heads > kMaxCtas / std::max(p->nsplit, 4)) return BA_ERR_UNSUPPORTED;
+  p->nsplit = p->row_tile == 256 ? paged_chunk_splits(*p, sm_count()) : paged_decode_splits(*p, sm_count());
+  if (tiles * p->B * p->cache.heads > kMaxCtas / std::max(p->nsplit, p->row_tile / 8)) return BA_ERR_UNSUPPORTED;
   if (p->nsplit > 1) {
     const size_t n = static_cast<size_t>(p->nsplit) * p->T * p->heads;
     *ws = align_up(n * p->cache.dp * 4) + align_up(n * 8);
@@ -176,7 +178,8 @@ ba_status ba_attention_paged(const void* q, int64_t q_stride_t, int64_t q_stride
   p.o = o;
   p.o_dt = o_dt;
   p.lse = lse;
-  return report_cuda(launch_paged_decode(p, dt, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+  return report_cuda(p.row_tile == 256 ? launch_paged_chunk(p, dt, st_) : launch_paged_decode(p, dt, st_));
 }
 
 }  // extern "C"

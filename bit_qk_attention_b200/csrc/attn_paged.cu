@@ -43,31 +43,11 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
-
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -90,17 +70,6 @@ __device__ __forceinline__ void codes_to_half(uint32_t wa, uint32_t wb, uint32_t
     const __half2 y = __hadd2(*reinterpret_cast<const __half2*>(&x[i]), bias);
     h[i] = *reinterpret_cast<const uint32_t*>(&y);
   }
-}
-
-// CTA index -> sequence, row tile, KV head and one of n parts.
-__device__ __forceinline__ void cta_of(const PagedAttnParams& p, unsigned idx, int n, int& b, int& tile, int& head,
-                                       int& part) {
-  part = idx % n;
-  idx /= n;
-  head = idx % p.cache.heads;
-  idx /= p.cache.heads;
-  tile = idx % p.row_tiles;
-  b = idx / p.row_tiles;
 }
 
 // Shared memory of a warp's stage: V rows of kRow bytes (16-byte pieces permuted, see v_piece),
@@ -147,19 +116,12 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(PagedAttnParams 
   // in it of the 16 tokens (l % 2) of the block l / 2 from `base` on: 16 blocks at a time.
   const int nmine = max(0, (v1 - v0 - warp + kWarps - 1) / kWarps);
   const int32_t* table = p.table + b * p.table_stride;
-  int pg = -1, po = 0;
+  PageAt at{-1, 0};
   auto look_up = [&](int base) {
     const int n = base + (lane >> 1);
-    pg = -1;
-    if (n < nmine) {
-      const int j = w.block_at(v0 + warp + n * kWarps) * kBlk + (lane & 1) * kPageUnit;
-      if (j < w.kv) {
-        const int e = j / cv.page_size;
-        pg = table[e];
-        po = j - e * cv.page_size;
-        if (pg < 0 || pg >= cv.num_pages) pg = -1;
-      }
-    }
+    at.page = -1;
+    if (n < nmine)
+      at = page_at(p, table, w.kv, w.block_at(v0 + warp + n * kWarps) * kBlk + (lane & 1) * kPageUnit);
   };
   uint32_t seen = 0;  // two bits per stage: which halves of the block have a page
   auto issue = [&](int n) {
@@ -170,8 +132,8 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(PagedAttnParams 
       uint32_t ok2 = 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int page = __shfl_sync(0xffffffffu, pg, 2 * (n & 15) + h);
-        const int off = __shfl_sync(0xffffffffu, po, 2 * (n & 15) + h);
+        const int page = __shfl_sync(0xffffffffu, at.page, 2 * (n & 15) + h);
+        const int off = __shfl_sync(0xffffffffu, at.off, 2 * (n & 15) + h);
         const bool ok = page >= 0;
         ok2 |= (ok ? 1u : 0u) << h;
         const uint8_t* blk = ok ? cv.block(page, head) : cv.data;
@@ -453,16 +415,7 @@ cudaError_t launch_decode(const PagedAttnParams& p, cudaStream_t s) {
   const int64_t tiles = static_cast<int64_t>(p.B) * p.row_tiles * p.cache.heads;
   kernel<<<static_cast<unsigned>(tiles * p.nsplit), kThreads, smem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess || p.nsplit == 1) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * 2 * NR));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel, p, 2 * NR, kBlk, kMinBlocks);
+  return launch_paged_join(p, kBlk, kMinBlocks, s);
 }
 
 template <typename T>
@@ -472,6 +425,21 @@ cudaError_t launch_decode_t(const PagedAttnParams& p, cudaStream_t s) {
 }
 
 }  // namespace
+
+cudaError_t launch_paged_join(const PagedAttnParams& p, int bk, int min_blocks, cudaStream_t s) {
+  // A CTA joins two rows per warp.
+  const int per_tile = p.row_tile / (2 * kWarps);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.B) * p.row_tiles * p.cache.heads * per_tile));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel, p, per_tile, bk, min_blocks);
+}
 
 cudaError_t launch_paged_decode(const PagedAttnParams& p, int dt, cudaStream_t s) {
   return dt == BA_F16 ? launch_decode_t<__half>(p, s) : launch_decode_t<__nv_bfloat16>(p, s);

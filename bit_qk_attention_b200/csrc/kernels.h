@@ -89,5 +89,6 @@ ba_status report_cuda(cudaError_t e);
 
 // Device status word of the kernels with bounded waits.
 cudaError_t read_and_clear_device_status(int* value, cudaStream_t s);
+cudaError_t read_and_clear_paged_status(int* value, cudaStream_t s);
 
 }  // namespace binattn

@@ -108,9 +108,65 @@ __device__ __forceinline__ int splits_used(int nsplit, int nblk, int min_blocks)
   return max(1, min(nsplit, nblk / min_blocks));
 }
 
+// Page of the 16 tokens from j on (a multiple of 16) and their offset in it; page -1 where there is
+// none: behind the sequence, or outside the cache.
+struct PageAt {
+  int page, off;
+};
+
+__device__ __forceinline__ PageAt page_at(const PagedAttnParams& p, const int32_t* table, int kv, int j) {
+  PageAt at{-1, 0};
+  if (j < kv) {
+    const int e = j / p.cache.page_size;
+    at.page = table[e];
+    at.off = j - e * p.cache.page_size;
+    if (at.page < 0 || at.page >= p.cache.num_pages) at.page = -1;
+  }
+  return at;
+}
+
+// CTA index -> sequence, row tile, KV head and one of n parts.
+__device__ __forceinline__ void cta_of(const PagedAttnParams& p, unsigned idx, int n, int& b, int& tile, int& head,
+                                       int& part) {
+  part = idx % n;
+  idx /= n;
+  head = idx % p.cache.heads;
+  idx /= p.cache.heads;
+  tile = idx % p.row_tiles;
+  b = idx / p.row_tiles;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
 cudaError_t launch_paged_decode(const PagedAttnParams& p, int dt, cudaStream_t s);
 // Parts of the key axis that the kernel is launched with on this device.
 int paged_decode_splits(const PagedAttnParams& p, int sms);
+cudaError_t launch_paged_chunk(const PagedAttnParams& p, int dt, cudaStream_t s);
+int paged_chunk_splits(const PagedAttnParams& p, int sms);
+// Second kernel of a split launch: joins the parts of the row tiles (key blocks of bk tokens, at
+// least min_blocks of them per part).
+cudaError_t launch_paged_join(const PagedAttnParams& p, int bk, int min_blocks, cudaStream_t s);
 
 cudaError_t launch_cache_write(const CacheWriteParams& p, int dt, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheReadParams& p, int dt, cudaStream_t s);
