@@ -81,8 +81,11 @@ ba_status plan(const ba_kv_cache* cache, const ba_paged_seqs* s, PagedAttnParams
   const int64_t tiles = ceil_div(rows, p->row_tile);
   if (tiles > kMaxCtas / (static_cast<int64_t>(p->B) * p->cache.heads)) return BA_ERR_UNSUPPORTED;
   p->row_tiles = static_cast<int>(tiles);
-  p->nsplit = p->row_tile == 256 ? paged_chunk_splits(*p, sm_count()) : paged_decode_splits(*p, sm_count());
-  if (tiles * p->B * p->cache.heads > kMaxCtas / std::max(p->nsplit, p->row_tile / 8)) return BA_ERR_UNSUPPORTED;
+  int blocks = 0;
+  p->split_blocks = p->row_tile == 256 ? paged_chunk_split_blocks(*p, sm_count(), &blocks)
+                                       : paged_decode_split_blocks(*p, sm_count(), &blocks);
+  p->nsplit = std::max(1, static_cast<int>(ceil_div(blocks, p->split_blocks)));
+  if (tiles * p->B * p->cache.heads > kMaxCtas / std::max(p->nsplit, p->row_tile)) return BA_ERR_UNSUPPORTED;
   if (p->nsplit > 1) {
     const size_t n = static_cast<size_t>(p->nsplit) * p->T * p->heads;
     *ws = align_up(n * p->cache.dp * 4) + align_up(n * 8);

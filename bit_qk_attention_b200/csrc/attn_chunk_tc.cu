@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
   cta_of(p, gridDim.x - 1 - blockIdx.x, p.nsplit, b, tile, head, split);
   const RowTile w = row_tile(p, b, tile, kBlk);
   if (w.rows <= 0) return;
-  const int used = splits_used(p.nsplit, w.nblk, kMinBlocks);
+  const int used = splits_used(p, w.nblk);
   if (split >= used) return;
   const int v0 = static_cast<int>(static_cast<int64_t>(w.nblk) * split / used);
   const int n_blk = static_cast<int>(static_cast<int64_t>(w.nblk) * (split + 1) / used) - v0;
@@ -512,7 +512,7 @@ cudaError_t launch_chunk(const PagedAttnParams& p, int dt, cudaStream_t s) {
   const int64_t grid = static_cast<int64_t>(p.B) * p.row_tiles * p.cache.heads * p.nsplit;
   kernel<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(p, dt == BA_F16 ? 1 : 0, wide ? 1 : 0);
   if ((e = cudaGetLastError()) != cudaSuccess || p.nsplit == 1) return e;
-  return launch_paged_join(p, kBlk, kMinBlocks, s);
+  return launch_paged_join(p, kBlk, s);
 }
 
 }  // namespace
@@ -521,12 +521,14 @@ cudaError_t launch_paged_chunk(const PagedAttnParams& p, int dt, cudaStream_t s)
   return p.cache.dp > 64 ? launch_chunk<128>(p, dt, s) : launch_chunk<64>(p, dt, s);
 }
 
-int paged_chunk_splits(const PagedAttnParams& p, int sms) {
+int paged_chunk_split_blocks(const PagedAttnParams& p, int sms, int* max_blocks) {
   int64_t keys = p.max_kv_len;
   if (p.causal && p.window > 0)
     keys = std::min<int64_t>(keys, static_cast<int64_t>(p.window) + p.row_tile / p.group + p.sinks + 2 * kBlk);
   const int64_t blocks = ceil_div(keys, kBlk), tiles = static_cast<int64_t>(p.B) * p.row_tiles * p.cache.heads;
-  return static_cast<int>(std::max<int64_t>(1, std::min(sms / tiles, blocks / kMinBlocks)));
+  *max_blocks = static_cast<int>(blocks);
+  const int64_t parts = std::max<int64_t>(1, std::min(sms / tiles, blocks / kMinBlocks));
+  return static_cast<int>(std::max<int64_t>(1, ceil_div(blocks, parts)));
 }
 
 cudaError_t read_and_clear_paged_status(int* value, cudaStream_t s) {

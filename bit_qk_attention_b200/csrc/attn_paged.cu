@@ -1,21 +1,26 @@
 // Attention of few query rows over the paged cache (sm_100a): decoding and drafts.
 //
 // With few rows per KV head the kernel is bound by reading the cache once: dp + 19 bytes per token
-// and head. The work is laid out so that the arithmetic stays beside those loads:
+// and head, and at HBM's rate a key of 147 bytes leaves an SM some 6.5 cycles. So the work per key
+// is kept small:
 //   * A CTA takes one sequence, one KV head, up to 8 NR rows (new tokens x heads of the group, which
 //     share every key) and a part of the key axis. Each of its warps walks 32-key blocks of its own
 //     through a ring of cp.async stages, with no synchronisation between warps until the end.
-//   * Scores are XOR / popc on the CUDA cores: x = d - 2 popc, s = (scale mu_q mu_j log2 e) x, one
-//     (key, row) pair per thread, placed so that the weights are the B fragment of the product.
-//   * P.V runs on the tensor cores as V^T P^T (mma.sync m16n8k16, fp16 in, fp32 out): 16 channels x
-//     16 keys of V against 16 keys x 8 rows, so that 8 rows fill the instruction (a 128-row
-//     tcgen05 tile would be mostly empty, and the kernel waits for memory, not for the product).
-//     The codes are whole numbers, exact in fp16; the order of the channels in a fragment is chosen
-//     so that a thread's channels are neighbours in memory.
+//   * Scores are products of whole numbers on the tensor cores (mma.sync m16n8k32, int8). With K's
+//     sign bits k in {0, 1} and Q in {-1, +1}, x = sum q - 2 sum q k. The bits need no expanding: a
+//     word masked by 0x01010101 << s holds four of them as bytes of value 2^s, and the byte of Q that
+//     meets it holds 2^(6 - s), so that every product is 64 q k. (XOR and popc per (key, row) pair
+//     took three times the instructions for 8 rows.) The accumulators start at the bit pattern of
+//     1.5 * 2^23, which makes the whole-number result a float as it is.
+//   * P.V runs as V^T P^T (mma.sync m16n8k16, fp16 in, fp32 out): 16 channels x 16 keys of V against
+//     16 keys x 8 rows, so that 8 rows fill the instruction (a 128-row tcgen05 tile would be mostly
+//     empty). ldmatrix transposes the bytes; two instructions make a pair of them fp16 numbers.
 //   * A value row's exponent e_j joins the score instead of the codes: the weight is
 //     2^(s_j + e_j - M) with M the running maximum of s_j + e_j, and the softmax sum adds
 //     weight * 2^-e_j. M moves (and the sums are rescaled) only when a score passes it by more than
 //     2^8, so that most blocks rescale nothing; the weights then reach 2^8, far inside fp16.
+//   * Weights are rounded to fp16 (2^-11 of each), which disappears in a bf16 result. For fp16 and
+//     fp32 results a second product adds what the first rounding left off (EXACT).
 //   * Parts of the key axis leave (M, sum, unnormalised o) in fp32, joined by a second kernel that
 //     is launched as a programmatic dependent. Short sequences use fewer parts, down to one, which
 //     writes the result itself.
@@ -32,10 +37,11 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kBlk = 32;        // keys per stage of a warp
+constexpr int kBlk = 32;       // keys per stage of a warp
 constexpr int kStages = 3;
-constexpr int kMinBlocks = 16;  // blocks (of 32 keys) a split takes at least
 constexpr float kSlack = 8.0f;  // log2 by which scores may pass the running maximum
+constexpr int kMagicBits = 0x4B400000;  // 1.5 * 2^23
+constexpr float kMagic = 12582912.0f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -43,92 +49,136 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  const uint4 u = lds128(a);
+  return make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void sts_f32(uint32_t a, float x) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
+}
+
+// c += A B, A 16 x 32 signed bytes (rows g and g + 8 of Q), B 32 x 8 unsigned bytes (keys).
+__device__ __forceinline__ void mma_qk(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Codes of two keys (4 channels each, biased by 128) -> fp16 pairs (key 0, key 1) of each channel.
-// A byte u under the exponent of 1024 reads 1024 + u, so 1024 + u - 1152 is the signed code.
-__device__ __forceinline__ void codes_to_half(uint32_t wa, uint32_t wb, uint32_t (&h)[4]) {
-  wa ^= 0x80808080u;
-  wb ^= 0x80808080u;
-  const uint32_t lo = __byte_perm(wa, wb, 0x5140), hi = __byte_perm(wa, wb, 0x7362);
-  const uint32_t x[4] = {__byte_perm(lo, 0x64646464u, 0x4140), __byte_perm(lo, 0x64646464u, 0x4342),
-                         __byte_perm(hi, 0x64646464u, 0x4140), __byte_perm(hi, 0x64646464u, 0x4342)};
-  const __half2 bias = __floats2half2_rn(-1152.0f, -1152.0f);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 y = __hadd2(*reinterpret_cast<const __half2*>(&x[i]), bias);
-    h[i] = *reinterpret_cast<const uint32_t*>(&y);
-  }
+// c += A B, A 16 channels x 16 keys of V, B 16 keys x 8 rows of P.
+__device__ __forceinline__ void mma_pv(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Shared memory of a warp's stage: V rows of kRow bytes (16-byte pieces permuted, see v_piece),
-// sign rows, mu, exponents.
-template <int CPG>  // channels per fragment row group: 16 (rows of 128 bytes) or 8 (rows of 64)
-struct Stage {
+// Two 16 x 16 matrices of bytes, transposed. Lanes 0-15 and 16-31 give the rows' addresses; the lane
+// (g, t) gets, of each matrix, columns g and g + 8 of rows 4 t .. 4 t + 3.
+__device__ __forceinline__ void ldmatrix_t8(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+
+// Four codes -> two fp16 pairs (bytes 0 and 1, bytes 2 and 3). A byte u = code + 128 under the
+// exponent of 1024 reads 1024 + u, and 1024 + u - 1152 is the code.
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  w ^= 0x80808080u;
+  const uint32_t x[2] = {__byte_perm(w, 0x64646464u, 0x4140), __byte_perm(w, 0x64646464u, 0x4342)};
+  const __half2 bias = __floats2half2_rn(-1152.0f, -1152.0f);
+  const __half2 a = __hadd2(*reinterpret_cast<const __half2*>(&x[0]), bias);
+  const __half2 b = __hadd2(*reinterpret_cast<const __half2*>(&x[1]), bias);
+  lo = *reinterpret_cast<const uint32_t*>(&a);
+  hi = *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Shared memory of a warp: stages of V rows of kRow bytes (16-byte pieces permuted), sign rows, mu,
+// exponents; then what the scores of one block need per key as floats: mu, e, 2^-e.
+template <int CPG>  // eighths of the channels: 16 (rows of 128 bytes) or 8 (rows of 64)
+struct Ring {
   static constexpr int kRow = CPG * 8;
   static constexpr int offBits = kBlk * kRow;
   static constexpr int offMu = offBits + kBlk * 16;
   static constexpr int offExp = offMu + kBlk * 2;
-  static constexpr int kBytes = offExp + kBlk;
-  // Byte offset of the 16-byte piece c of key j. A warp's load of the fragment rows touches keys
-  // 2t (t = 0..3) and neighbouring pieces: moving the pieces of key j by 2 ((j / 2) % 4) puts them
-  // into different banks.
-  static __device__ __forceinline__ int v_piece(int j, int c) {
-    return ((j * (kRow / 16) + c) ^ (2 * ((j >> 1) & 3))) * 16;
+  static constexpr int kStage = offExp + kBlk;
+  static constexpr int offF = kStages * kStage;
+  static constexpr int kBytes = offF + 3 * kBlk * 4;
+  // Byte offset of the 16-byte piece c of key j: eight neighbouring keys' pieces c lie in
+  // different banks.
+  static __device__ __forceinline__ int piece(int j, int c) {
+    return kRow == 128 ? (j * 8 + (c ^ (j & 7))) * 16 : (j * 4 + (c ^ ((j >> 1) & 3))) * 16;
   }
 };
 
-template <typename T, int CPG, int NR>
-__global__ void __launch_bounds__(kThreads) paged_decode_kernel(PagedAttnParams p) {
-  using S = Stage<CPG>;
-  constexpr int MT = CPG / 2;   // 16-channel tiles
-  constexpr int R = 8 * NR;     // rows of a CTA
-  constexpr int CH = CPG * 8;   // channels of the accumulators (>= d)
+// One row of q by a warp: sign words and sum of |x|.
+template <typename T>
+__device__ __forceinline__ void scan_row(const T* src, int d, int lane, uint32_t (&word)[4], float& sum) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int c = 32 * k + lane;
+    const float x = c < d ? load1<T>(src + c) : 0.0f;
+    word[k] = __ballot_sync(0xffffffffu, x < 0.0f);
+    sum += fabsf(x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+}
+
+template <int CPG, int NR, bool EXACT>
+__global__ void __launch_bounds__(kThreads) paged_decode_kernel(PagedAttnParams p, int q_f16) {
+  using S = Ring<CPG>;
+  constexpr int MT = CPG / 2;  // 16-channel tiles
+  constexpr int R = 8 * NR;    // rows of a CTA
+  constexpr int CH = CPG * 8;  // channels of the accumulators (>= d)
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint4 s_bits[R];
+  __shared__ uint32_t s_bits[R][4];
   __shared__ float s_mu[R];
   __shared__ float2 s_ml[kWarps][R];
 
+  allow_dependents();
   const CacheView& cv = p.cache;
   int b, tile, head, split;
   cta_of(p, blockIdx.x, p.nsplit, b, tile, head, split);
   const RowTile w = row_tile(p, b, tile, kBlk);
   if (w.rows <= 0) return;
-  const int used = splits_used(p.nsplit, w.nblk, kMinBlocks);
+  const int used = splits_used(p, w.nblk);
   if (split >= used) return;
   const int v0 = static_cast<int>(static_cast<int64_t>(w.nblk) * split / used);
   const int v1 = static_cast<int>(static_cast<int64_t>(w.nblk) * (split + 1) / used);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * kStages * S::kBytes;
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S::kBytes;
 
   // The warp's blocks are v0 + warp, v0 + warp + kWarps, ... Lane l keeps the page and the offset
-  // in it of the 16 tokens (l % 2) of the block l / 2 from `base` on: 16 blocks at a time.
+  // in it of the 16 tokens (l % 2) of the block l / 2 after the last look-up: 16 blocks at a time.
   const int nmine = max(0, (v1 - v0 - warp + kWarps - 1) / kWarps);
   const int32_t* table = p.table + b * p.table_stride;
   PageAt at{-1, 0};
-  auto look_up = [&](int base) {
-    const int n = base + (lane >> 1);
-    at.page = -1;
-    if (n < nmine)
-      at = page_at(p, table, w.kv, w.block_at(v0 + warp + n * kWarps) * kBlk + (lane & 1) * kPageUnit);
-  };
   uint32_t seen = 0;  // two bits per stage: which halves of the block have a page
-  auto issue = [&](int n) {
+  constexpr int PPR = S::kRow / 16;   // pieces of a V row
+  constexpr int RPI = 32 / PPR;       // rows that the warp copies per instruction
+  const int vrow = lane / PPR, vcol = lane % PPR;
+  const bool vok = vcol * 16 < cv.dp;
+  const int vsrc = vrow * cv.dp + vcol * 16, vstep = RPI * cv.dp;
+  // The half's other pieces: 16 sign rows, two pieces of mu, one of exponents.
+  const int xsrc = lane < 16 ? cv.off_bits() + lane * 16 : (lane < 18 ? cv.off_mu() + (lane - 16) * 16 : cv.off_exp());
+  const int xmul = lane < 16 ? 16 : (lane < 18 ? 2 : 1);
+  const uint32_t xdst = lane < 16 ? S::offBits + lane * 16 : (lane < 18 ? S::offMu + (lane - 16) * 16 : S::offExp);
+  const uint32_t xhalf = kPageUnit * xmul;
+  auto issue = [&](int n, int st) {
     if (n < nmine) {
-      if ((n & 15) == 0) look_up(n);
-      const int st = n % kStages;
-      const uint32_t dst = ring + st * S::kBytes;
+      if ((n & 15) == 0) {
+        at.page = -1;
+        const int m = n + (lane >> 1);
+        if (m < nmine) at = page_at(p, table, w.kv, w.block_at(v0 + warp + m * kWarps) * kBlk + (lane & 1) * kPageUnit);
+      }
+      const uint32_t dst = ring + st * S::kStage;
       uint32_t ok2 = 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -136,65 +186,63 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(PagedAttnParams 
         const int off = __shfl_sync(0xffffffffu, at.off, 2 * (n & 15) + h);
         const bool ok = page >= 0;
         ok2 |= (ok ? 1u : 0u) << h;
+        // Where there is no page nothing is read and the stage gets zeros.
         const uint8_t* blk = ok ? cv.block(page, head) : cv.data;
-        constexpr int PPR = S::kRow / 16;  // pieces of a row
+        const uint8_t* src = blk + (ok ? off * cv.dp + vsrc : 0);
+        const int step = ok ? vstep : 0;
+        if (vok) {
 #pragma unroll
-        for (int i = 0; i < kPageUnit * PPR / 32; ++i) {
-          const int idx = lane + 32 * i, j = idx / PPR, c = idx % PPR;
-          if (c * 16 < cv.dp)
-            cp_async16(dst + S::v_piece(kPageUnit * h + j, c), ok ? blk + (off + j) * cv.dp + c * 16 : blk, ok);
+          for (int i = 0; i < kPageUnit / RPI; ++i)
+            cp_async16(dst + S::piece(kPageUnit * h + i * RPI + vrow, vcol), src + i * step, ok);
         }
-        // The half's other pieces: 16 sign rows, two pieces of mu, one of exponents.
-        if (lane < 19) {
-          const uint8_t* src = lane < 16 ? blk + cv.off_bits() + (off + lane) * 16
-                                         : (lane < 18 ? blk + cv.off_mu() + off * 2 + (lane - 16) * 16
-                                                      : blk + cv.off_exp() + off);
-          const uint32_t to = lane < 16 ? S::offBits + (kPageUnit * h + lane) * 16
-                                        : (lane < 18 ? S::offMu + kPageUnit * h * 2 + (lane - 16) * 16
-                                                     : S::offExp + kPageUnit * h);
-          cp_async16(dst + to, ok ? src : blk, ok);
-        }
+        if (lane < 19) cp_async16(dst + xdst + h * xhalf, blk + (ok ? xsrc + off * xmul : 0), ok);
       }
       seen = (seen & ~(3u << (2 * st))) | (ok2 << (2 * st));
     }
     cp_async_commit();
   };
 #pragma unroll
-  for (int n = 0; n < kStages - 1; ++n) issue(n);
+  for (int n = 0; n < kStages - 1; ++n) issue(n, n);
 
   // Sign bits and scale of the rows, while the first blocks are on their way.
   for (int r = warp; r < R; r += kWarps) {
-    uint4 bits = make_uint4(0u, 0u, 0u, 0u);
+    uint32_t word[4] = {0u, 0u, 0u, 0u};
     float sum = 0.0f;
     if (r < w.rows) {
       const int i = (w.r0 + r) / p.group, hq = head * p.group + (w.r0 + r) % p.group;
-      const T* src = static_cast<const T*>(p.q) + (w.t0 + i) * p.q_stride_t + hq * p.q_stride_h;
-      uint32_t word[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int c = 32 * k + lane;
-        const float x = c < cv.d ? load1<T>(src + c) : 0.0f;
-        word[k] = __ballot_sync(0xffffffffu, x < 0.0f);
-        sum += fabsf(x);
-      }
-      bits = make_uint4(word[0], word[1], word[2], word[3]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const int64_t src = (w.t0 + i) * p.q_stride_t + hq * p.q_stride_h;
+      if (q_f16)
+        scan_row(static_cast<const __half*>(p.q) + src, cv.d, lane, word, sum);
+      else
+        scan_row(static_cast<const __nv_bfloat16*>(p.q) + src, cv.d, lane, word, sum);
     }
-    if (lane == 0) {
-      s_bits[r] = bits;
-      s_mu[r] = sum / static_cast<float>(cv.d);
-    }
+    if (lane < 4) s_bits[r][lane] = lane == 0 ? word[0] : (lane == 1 ? word[1] : (lane == 2 ? word[2] : word[3]));
+    if (lane == 0) s_mu[r] = sum / static_cast<float>(cv.d);
   }
   __syncthreads();
 
-  uint4 qb[NR];
-  float cq[NR];
+  // Q as the A operand: this thread's bytes meet word t of the keys; byte i of step s is channel
+  // 32 t + 8 i + s, and holds +-2^(6 - s) (s = 7: +-1, its bit is moved down by one).
+  uint32_t qa[NR][8];
+  float cq[NR], qsum[NR];
   int last[NR], wlo[NR];  // the row sees keys j <= last with j >= wlo or j < sinks
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
     const int r = 8 * n + g;
-    qb[n] = s_bits[r];
+    const uint32_t word = s_bits[r][t];
+#pragma unroll
+    for (int st = 0; st < 8; ++st) {
+      uint32_t x = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = 8 * i + st;
+        const int mag = 32 * t + c < cv.d ? 1 << (st == 7 ? 0 : 6 - st) : 0;
+        x |= (static_cast<uint32_t>((word >> c) & 1u ? -mag : mag) & 0xffu) << (8 * i);
+      }
+      qa[n][st] = x;
+    }
+    const int neg = __popc(s_bits[r][0]) + __popc(s_bits[r][1]) + __popc(s_bits[r][2]) + __popc(s_bits[r][3]);
+    qsum[n] = static_cast<float>(cv.d - 2 * neg);
     cq[n] = p.scale_log2 * s_mu[r];
     const int pos = w.pos0() + (w.r0 + r) / p.group;
     last[n] = r < w.rows ? (p.causal ? min(pos, w.kv - 1) : w.kv - 1) : -1;
@@ -205,63 +253,101 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(PagedAttnParams 
   const int all_lo = p.causal && p.window > 0 ? w.pos0() + (w.r0 + w.rows - 1) / p.group - p.window + 1 : 0;
 
   float acc[NR][MT][4];
-  float M[NR], l[NR];
+  float M[NR];
+  float2 l[NR];
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
     M[n] = -CUDART_INF_F;
-    l[n] = 0.0f;
+    l[n] = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][m][i] = 0.0f;
   }
-  const float dfl = static_cast<float>(cv.d);
+  // Key of column g of the first of two score products of 16 keys (the second: two further on), such
+  // that a thread's four scores are the keys 4 t .. 4 t + 3.
+  const uint32_t kword = (4 * (g >> 1) + (g & 1)) * 16 + 4 * t;
+  const uint32_t vlane = (lane & 15), vpiece = lane >> 4;
 
+  int st = 0;
   for (int n = 0; n < nmine; ++n) {
     cp_async_wait<kStages - 2>();
     __syncwarp();
-    issue(n + kStages - 1);  // into the stage that the block before this one has left
-    const int st = n % kStages;
-    const uint32_t src = ring + st * S::kBytes;
+    issue(n + kStages - 1, st == 0 ? kStages - 1 : st - 1);  // into the stage that the last block left
+    const uint32_t src = ring + st * S::kStage, fl = ring + S::offF;
     const int j0 = w.block_at(v0 + warp + n * kWarps) * kBlk;
     const uint32_t ok2 = (seen >> (2 * st)) & 3u;
-    const bool whole = ok2 == 3u && j0 + kBlk - 1 <= all_last && j0 >= all_lo;
-
-    // Scores s + e of this thread's 8 keys: key(u) = 16 (u / 4) + 2 t + {0, 1, 8, 9}[u % 4].
-    float sc[NR][8], down[8];  // down = 2^-e
+    st = st == kStages - 1 ? 0 : st + 1;
+    {
+      const int e = static_cast<int8_t>(lds16(src + S::offExp + (lane & ~1)) >> (8 * (lane & 1)));
+      const int ec = min(max(e, kMinExp), kMaxExp);
+      sts_f32(fl + 4 * lane, __uint_as_float(lds16(src + S::offMu + 2 * lane) << 16));
+      sts_f32(fl + 4 * (kBlk + lane), static_cast<float>(ec));
+      sts_f32(fl + 4 * (2 * kBlk + lane), __uint_as_float(static_cast<uint32_t>(127 - ec) << 23));
+    }
+    // 64 sum q k of 16 keys each (h), keys 4 t .. 4 t + 3 of them in the order 0, 1 | 2, 3.
+    int x[2][2][4];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int key = 16 * (u >> 2) + 2 * t + (u & 1) + 8 * ((u >> 1) & 1);
-      const uint4 kb = lds128(src + S::offBits + key * 16);
-      const float mu = __uint_as_float(lds16(src + S::offMu + key * 2) << 16);
-      const int e = min(max(static_cast<int>(static_cast<int8_t>(lds16(src + S::offExp + (key & ~1)) >> (8 * (key & 1)))),
-                            kMinExp), kMaxExp);
-      down[u] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const int diff = __popc(qb[r].x ^ kb.x) + __popc(qb[r].y ^ kb.y) + __popc(qb[r].z ^ kb.z) + __popc(qb[r].w ^ kb.w);
-        const float x = __fmaf_rn(-2.0f, static_cast<float>(diff), dfl);
-        sc[r][u] = __fmaf_rn(cq[r] * mu, x, static_cast<float>(e));
-        if (!whole) {
-          const int j = j0 + key;
-          const bool see = ((ok2 >> (u >> 2)) & 1u) && j <= last[r] && (j >= wlo[r] || j < p.sinks);
-          if (!see) sc[r][u] = -CUDART_INF_F;
-        }
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t word = lds32(src + S::offBits + kword + (16 * h + 2 * k) * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[h][k][i] = kMagicBits;
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          mma_qk(x[h][k], qa[0][2 * s], NR == 2 ? qa[NR - 1][2 * s] : 0u, qa[0][2 * s + 1],
+                 NR == 2 ? qa[NR - 1][2 * s + 1] : 0u, word & (0x01010101u << (2 * s)),
+                 s == 3 ? (word >> 1) & 0x40404040u : word & (0x02020202u << (2 * s)));
       }
+    __syncwarp();
+    // Scores + e: sc[r][h][k] holds the keys 16 h + 4 t + 2 k and the next.
+    float2 sc[NR][2][2], down[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 mu = lds_f4(fl + 64 * h + 16 * t), e = lds_f4(fl + 4 * kBlk + 64 * h + 16 * t),
+                   dn = lds_f4(fl + 8 * kBlk + 64 * h + 16 * t);
+      const float2 mu2[2] = {make_float2(mu.x, mu.y), make_float2(mu.z, mu.w)};
+      const float2 e2[2] = {make_float2(e.x, e.y), make_float2(e.z, e.w)};
+      down[h][0] = make_float2(dn.x, dn.y);
+      down[h][1] = make_float2(dn.z, dn.w);
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          // x = sum q - 2 sum q k: exact, the constant of the accumulator's start taken off with it.
+          const float back = qsum[r] + kMagic / 32.0f;
+          const float2 y = __ffma2_rn(make_float2(__int_as_float(x[h][k][2 * r]), __int_as_float(x[h][k][2 * r + 1])),
+                                      make_float2(-0.03125f, -0.03125f), make_float2(back, back));
+          sc[r][h][k] = __ffma2_rn(__fmul2_rn(y, mu2[k]), make_float2(cq[r], cq[r]), e2[k]);
+        }
+    }
+    if (!(ok2 == 3u && j0 + kBlk - 1 <= all_last && j0 >= all_lo)) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int j = j0 + 16 * h + 4 * t + k;
+            const bool see = ((ok2 >> h) & 1u) && j <= last[r] && (j >= wlo[r] || j < p.sinks);
+            float& v = (k & 1) ? sc[r][h][k >> 1].y : sc[r][h][k >> 1].x;
+            if (!see) v = -CUDART_INF_F;
+          }
     }
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      float mx = sc[r][0];
-#pragma unroll
-      for (int u = 1; u < 8; ++u) mx = fmaxf(mx, sc[r][u]);
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const bool moves = mx > M[r] + kSlack;
-      if (__any_sync(0xffffffffu, moves)) {
+      float mx = fmaxf(fmaxf(fmaxf(sc[r][0][0].x, sc[r][0][0].y), fmaxf(sc[r][0][1].x, sc[r][0][1].y)),
+                       fmaxf(fmaxf(sc[r][1][0].x, sc[r][1][0].y), fmaxf(sc[r][1][1].x, sc[r][1][1].y)));
+      if (__any_sync(0xffffffffu, mx > M[r] + kSlack)) {
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const bool moves = mx > M[r] + kSlack;
         const float to = moves ? mx : M[r];
         const float f = M[r] == -CUDART_INF_F ? 0.0f : ex2(M[r] - to);
         M[r] = to;
-        l[r] *= f;
+        l[r].x *= f;
+        l[r].y *= f;
         const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -271,48 +357,47 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(PagedAttnParams 
           acc[r][m][3] *= f1;
         }
       }
-      const float ref = M[r] == -CUDART_INF_F ? 0.0f : M[r];
+      const float ref = M[r] == -CUDART_INF_F ? 0.0f : -M[r];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        sc[r][u] = ex2(sc[r][u] - ref);
-        l[r] = __fmaf_rn(sc[r][u], down[u], l[r]);
-      }
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float2 y = __fadd2_rn(sc[r][h][k], make_float2(ref, ref));
+          sc[r][h][k] = make_float2(ex2(y.x), ex2(y.y));
+          l[r] = __ffma2_rn(sc[r][h][k], down[h][k], l[r]);
+        }
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t bf[NR][2];
+      uint32_t bf[NR][2], br[NR][2];
 #pragma unroll
       for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const __half2 x = __floats2half2_rn(sc[r][4 * h + 2 * k], sc[r][4 * h + 2 * k + 1]);
-          bf[r][k] = *reinterpret_cast<const uint32_t*>(&x);
+          const __half2 y = __floats2half2_rn(sc[r][h][k].x, sc[r][h][k].y);
+          bf[r][k] = *reinterpret_cast<const uint32_t*>(&y);
+          if (EXACT) {
+            const float2 f = __half22float2(y);
+            const __half2 z = __floats2half2_rn(sc[r][h][k].x - f.x, sc[r][h][k].y - f.y);
+            br[r][k] = *reinterpret_cast<const uint32_t*>(&z);
+          }
         }
-      uint32_t code[4][CPG / 4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int key = 16 * h + 2 * t + (k & 1) + 8 * (k >> 1);
-        if constexpr (CPG == 16) {
-          const uint4 x = lds128(src + S::v_piece(key, g));
-          code[k][0] = x.x;
-          code[k][1] = x.y;
-          code[k][2] = x.z;
-          code[k][3] = x.w;
-        } else {
-          const uint2 x = lds64(src + S::v_piece(key, g >> 1) + (g & 1) * 8);
-          code[k][0] = x.x;
-          code[k][1] = x.y;
-        }
-      }
+      for (int m = 0; m < MT; m += 2) {
+        if (16 * m < cv.dp) {
+          uint32_t code[4];
+          ldmatrix_t8(src + S::piece(kPageUnit * h + vlane, m + vpiece), code);
 #pragma unroll
-      for (int x = 0; x < CPG / 4; ++x) {
-        uint32_t ha[4], hb[4];
-        codes_to_half(code[0][x], code[1][x], ha);
-        codes_to_half(code[2][x], code[3][x], hb);
+          for (int k = 0; k < 2; ++k) {
+            uint32_t a[4];
+            codes_to_half(code[2 * k], a[0], a[2]);
+            codes_to_half(code[2 * k + 1], a[1], a[3]);
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          mma16816(acc[r][2 * x], ha[0], ha[1], hb[0], hb[1], bf[r][0], bf[r][1]);
-          mma16816(acc[r][2 * x + 1], ha[2], ha[3], hb[2], hb[3], bf[r][0], bf[r][1]);
+            for (int r = 0; r < NR; ++r) {
+              mma_pv(acc[r][m + k], a, bf[r][0], bf[r][1]);
+              if (EXACT) mma_pv(acc[r][m + k], a, br[r][0], br[r][1]);
+            }
+          }
         }
       }
     }
@@ -322,19 +407,19 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(PagedAttnParams 
   __syncthreads();
 
   // Join the warps: each leaves its (M, l) and its sums in shared memory. A thread holds, for the
-  // rows 8 n + 2 t and 8 n + 2 t + 1, the channels CPG g .. CPG g + CPG - 1.
+  // rows 8 n + 2 t and 8 n + 2 t + 1, the channels 16 m + g and 16 m + g + 8.
   float* s_o = reinterpret_cast<float*>(smem);  // [kWarps][R][CH]
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
-    l[n] += __shfl_xor_sync(0xffffffffu, l[n], 1);
-    l[n] += __shfl_xor_sync(0xffffffffu, l[n], 2);
-    if (t == 0) s_ml[warp][8 * n + g] = make_float2(M[n], l[n]);
+    float sum = l[n].x + l[n].y;
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    if (t == 0) s_ml[warp][8 * n + g] = make_float2(M[n], sum);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        *reinterpret_cast<float2*>(s_o + (warp * R + 8 * n + 2 * t + i) * CH + CPG * g + 2 * m) =
-            make_float2(acc[n][m][i], acc[n][m][2 + i]);
+      for (int i = 0; i < 4; ++i)
+        s_o[(warp * R + 8 * n + 2 * t + (i & 1)) * CH + 16 * m + g + 8 * (i >> 1)] = acc[n][m][i];
   }
   __syncthreads();
   for (int r = warp; r < w.rows; r += kWarps) {
@@ -348,13 +433,13 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(PagedAttnParams 
     }
     const int64_t row = (w.t0 + (w.r0 + r) / p.group) * p.heads + head * p.group + (w.r0 + r) % p.group;
     const float inv = used > 1 ? 1.0f : (lr > 0.0f ? 1.0f / lr : 0.0f);
-    for (int c = lane; c < cv.d; c += 32) {
+    for (int c = lane; c < cv.dp; c += 32) {
       float x = 0.0f;
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) x += f[k] * s_o[(k * R + r) * CH + c];
       if (used > 1)
         p.part_o[(split * p.T * p.heads + row) * cv.dp + c] = x;
-      else
+      else if (c < cv.d)
         store_out(p.o, row * cv.d + c, x * inv, p.o_dt);
     }
     if (lane == 0) {
@@ -364,73 +449,80 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(PagedAttnParams 
         p.lse[row] = lr > 0.0f ? (Mr + log2f(lr)) * CUDART_LN2_F : -CUDART_INF_F;
     }
   }
-  allow_dependents();
 }
 
-// Joins the parts of each row: o = sum_k 2^(M_k - M) o_k / sum_k 2^(M_k - M) l_k. One warp per row.
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(PagedAttnParams p, int per_tile, int bk, int min_blocks) {
+// Joins the parts of each row: o = sum_k 2^(M_k - M) o_k / sum_k 2^(M_k - M) l_k. One CTA per row: its
+// warps take every fourth part, four channels per lane, and meet in shared memory.
+__global__ void __launch_bounds__(kThreads) paged_join_kernel(PagedAttnParams p, int bk) {
+  __shared__ float s_x[kWarps][128];
+  __shared__ float s_l[kWarps];
   const CacheView& cv = p.cache;
-  int b, tile, head, part;
-  cta_of(p, blockIdx.x, per_tile, b, tile, head, part);
+  int b, tile, head, r;
+  cta_of(p, blockIdx.x, p.row_tile, b, tile, head, r);
   // Every CTA waits, also one with nothing to join: this grid must not complete before the one
   // whose parts it joins.
   grid_dependency_wait();
   const RowTile w = row_tile(p, b, tile, bk);
-  if (w.rows <= 0) return;
-  const int used = splits_used(p.nsplit, w.nblk, min_blocks);
+  if (r >= w.rows) return;
+  const int used = splits_used(p, w.nblk);
   if (used == 1) return;
-  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t all = p.T * p.heads;
-  for (int r = part * kWarps + (threadIdx.x >> 5); r < w.rows; r += per_tile * kWarps) {
-    const int64_t row = (w.t0 + (w.r0 + r) / p.group) * p.heads + head * p.group + (w.r0 + r) % p.group;
-    float M = -CUDART_INF_F;
-    for (int k = lane; k < used; k += 32) M = fmaxf(M, p.part_ml[k * all + row].x);
+  const int64_t row = (w.t0 + (w.r0 + r) / p.group) * p.heads + head * p.group + (w.r0 + r) % p.group;
+  float M = -CUDART_INF_F;
+  for (int k = lane; k < used; k += 32) M = fmaxf(M, p.part_ml[k * all + row].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float l = 0.0f, x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k = 0; k < used; ++k) {
-      const float2 ml = p.part_ml[k * all + row];
-      if (ml.x == -CUDART_INF_F) continue;
-      const float f = ex2(ml.x - M);
-      l = __fmaf_rn(f, ml.y, l);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < cv.d) x[i] = __fmaf_rn(f, p.part_o[(k * all + row) * cv.dp + lane + 32 * i], x[i]);
-    }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane + 32 * i < cv.d) store_out(p.o, row * cv.d + lane + 32 * i, x[i] * inv, p.o_dt);
-    if (lane == 0 && p.lse != nullptr) p.lse[row] = l > 0.0f ? (M + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float ref = M == -CUDART_INF_F ? 0.0f : M;
+  float l = 0.0f;
+  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const bool on = 4 * lane < cv.dp;
+#pragma unroll 4
+  for (int k = warp; k < used; k += kWarps) {
+    const float2 ml = p.part_ml[k * all + row];
+    const float4 o = on ? *reinterpret_cast<const float4*>(p.part_o + (k * all + row) * cv.dp + 4 * lane) : x;
+    const float f = ex2(ml.x - ref);
+    l = __fmaf_rn(f, ml.y, l);
+    x.x = __fmaf_rn(f, o.x, x.x);
+    x.y = __fmaf_rn(f, o.y, x.y);
+    x.z = __fmaf_rn(f, o.z, x.z);
+    x.w = __fmaf_rn(f, o.w, x.w);
   }
+  *reinterpret_cast<float4*>(&s_x[warp][4 * lane]) = x;
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  const float lt = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+  const int c = threadIdx.x;
+  if (c < cv.d) {
+    const float sum = s_x[0][c] + s_x[1][c] + s_x[2][c] + s_x[3][c];
+    store_out(p.o, row * cv.d + c, lt > 0.0f ? sum / lt : 0.0f, p.o_dt);
+  }
+  if (c == 0 && p.lse != nullptr) p.lse[row] = lt > 0.0f ? (M + log2f(lt)) * CUDART_LN2_F : -CUDART_INF_F;
 }
 
-template <typename T, int CPG, int NR>
-cudaError_t launch_decode(const PagedAttnParams& p, cudaStream_t s) {
-  constexpr int ring = kWarps * kStages * Stage<CPG>::kBytes, out = kWarps * 8 * NR * CPG * 8 * 4;
+template <int CPG, int NR, bool EXACT>
+cudaError_t launch_decode(const PagedAttnParams& p, int dt, cudaStream_t s) {
+  constexpr int ring = kWarps * Ring<CPG>::kBytes, out = kWarps * 8 * NR * CPG * 8 * 4;
   constexpr int smem = ring > out ? ring : out;
-  auto kernel = paged_decode_kernel<T, CPG, NR>;
+  auto kernel = paged_decode_kernel<CPG, NR, EXACT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(p.B) * p.row_tiles * p.cache.heads;
-  kernel<<<static_cast<unsigned>(tiles * p.nsplit), kThreads, smem, s>>>(p);
+  kernel<<<static_cast<unsigned>(tiles * p.nsplit), kThreads, smem, s>>>(p, dt == BA_F16 ? 1 : 0);
   if ((e = cudaGetLastError()) != cudaSuccess || p.nsplit == 1) return e;
-  return launch_paged_join(p, kBlk, kMinBlocks, s);
+  return launch_paged_join(p, kBlk, s);
 }
 
-template <typename T>
-cudaError_t launch_decode_t(const PagedAttnParams& p, cudaStream_t s) {
-  if (p.cache.dp > 64) return p.row_tile > 8 ? launch_decode<T, 16, 2>(p, s) : launch_decode<T, 16, 1>(p, s);
-  return p.row_tile > 8 ? launch_decode<T, 8, 2>(p, s) : launch_decode<T, 8, 1>(p, s);
+template <int CPG, int NR>
+cudaError_t launch_decode_o(const PagedAttnParams& p, int dt, cudaStream_t s) {
+  return p.o_dt == BA_BF16 ? launch_decode<CPG, NR, false>(p, dt, s) : launch_decode<CPG, NR, true>(p, dt, s);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_join(const PagedAttnParams& p, int bk, int min_blocks, cudaStream_t s) {
-  // A CTA joins two rows per warp.
-  const int per_tile = p.row_tile / (2 * kWarps);
+cudaError_t launch_paged_join(const PagedAttnParams& p, int bk, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.B) * p.row_tiles * p.cache.heads * per_tile));
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.B) * p.row_tiles * p.cache.heads * p.row_tile));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -438,21 +530,24 @@ cudaError_t launch_paged_join(const PagedAttnParams& p, int bk, int min_blocks, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel, p, per_tile, bk, min_blocks);
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel, p, bk);
 }
 
 cudaError_t launch_paged_decode(const PagedAttnParams& p, int dt, cudaStream_t s) {
-  return dt == BA_F16 ? launch_decode_t<__half>(p, s) : launch_decode_t<__nv_bfloat16>(p, s);
+  if (p.cache.dp > 64) return p.row_tile > 8 ? launch_decode_o<16, 2>(p, dt, s) : launch_decode_o<16, 1>(p, dt, s);
+  return p.row_tile > 8 ? launch_decode_o<8, 2>(p, dt, s) : launch_decode_o<8, 1>(p, dt, s);
 }
 
-int paged_decode_splits(const PagedAttnParams& p, int sms) {
-  // Keys that a tile can see, in blocks; four CTAs of a split fill an SM.
+int paged_decode_split_blocks(const PagedAttnParams& p, int sms, int* max_blocks) {
+  // Keys that a tile can see, in blocks. Four CTAs fill an SM: parts as small as it takes to fill
+  // the GPU, from one block per warp up to 2048 keys (a long sequence beside short ones should not
+  // leave its last CTA running alone).
   int64_t keys = p.max_kv_len;
   if (p.causal && p.window > 0)
     keys = std::min<int64_t>(keys, static_cast<int64_t>(p.window) + p.row_tile + p.sinks + 2 * kBlk);
   const int64_t blocks = ceil_div(keys, kBlk), tiles = static_cast<int64_t>(p.B) * p.row_tiles * p.cache.heads;
-  const int64_t want = ceil_div(static_cast<int64_t>(sms) * 4, tiles);
-  return static_cast<int>(std::max<int64_t>(1, std::min(want, blocks / kMinBlocks)));
+  *max_blocks = static_cast<int>(blocks);
+  return static_cast<int>(std::min<int64_t>(64, std::max<int64_t>(kWarps, ceil_div(blocks * tiles, static_cast<int64_t>(sms) * 4))));
 }
 
 }  // namespace binattn

@@ -57,7 +57,8 @@ struct PagedAttnParams {
   void* o;
   int o_dt;
   float* lse;
-  int nsplit;      // parts of the key axis (most)
+  int nsplit;       // parts of the key axis (most)
+  int split_blocks; // key blocks of a part (about)
   int row_tile;    // rows (token, head of the group) of a CTA's tile
   int row_tiles;   // tiles of a sequence and KV head (most)
   float* part_o;   // [nsplit][T * heads][dp] unnormalised sums, when nsplit > 1
@@ -103,9 +104,9 @@ __device__ __forceinline__ RowTile row_tile(const PagedAttnParams& p, int b, int
   return w;
 }
 
-// Splits that a tile of nblk blocks uses of the launch's nsplit: at least kMinSplit blocks each.
-__device__ __forceinline__ int splits_used(int nsplit, int nblk, int min_blocks) {
-  return max(1, min(nsplit, nblk / min_blocks));
+// Parts of the key axis that a tile of nblk blocks uses.
+__device__ __forceinline__ int splits_used(const PagedAttnParams& p, int nblk) {
+  return max(1, min(p.nsplit, static_cast<int>(ceil_div(nblk, p.split_blocks))));
 }
 
 // Page of the 16 tokens from j on (a multiple of 16) and their offset in it; page -1 where there is
@@ -160,13 +161,12 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 }
 
 cudaError_t launch_paged_decode(const PagedAttnParams& p, int dt, cudaStream_t s);
-// Parts of the key axis that the kernel is launched with on this device.
-int paged_decode_splits(const PagedAttnParams& p, int sms);
 cudaError_t launch_paged_chunk(const PagedAttnParams& p, int dt, cudaStream_t s);
-int paged_chunk_splits(const PagedAttnParams& p, int sms);
-// Second kernel of a split launch: joins the parts of the row tiles (key blocks of bk tokens, at
-// least min_blocks of them per part).
-cudaError_t launch_paged_join(const PagedAttnParams& p, int bk, int min_blocks, cudaStream_t s);
+// Key blocks of a part on a device of `sms` SMs, and the most blocks that a tile can have.
+int paged_decode_split_blocks(const PagedAttnParams& p, int sms, int* max_blocks);
+int paged_chunk_split_blocks(const PagedAttnParams& p, int sms, int* max_blocks);
+// Second kernel of a split launch: joins the parts of the row tiles (key blocks of bk tokens).
+cudaError_t launch_paged_join(const PagedAttnParams& p, int bk, cudaStream_t s);
 
 cudaError_t launch_cache_write(const CacheWriteParams& p, int dt, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheReadParams& p, int dt, cudaStream_t s);
