@@ -49,6 +49,18 @@ int sm_count() {
 
 size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
+// Regions of the workspace of a launch whose CTAs share the line of units; their size in bytes.
+size_t line_workspace(const PagedAttnParams& p, PagedAttnParams* out) {
+  const size_t n = static_cast<size_t>(p.ctas) * 2 * p.row_tile;
+  const size_t ml = align_up(n * p.cache.dp * 4), notes = ml + align_up(n * 8);
+  if (out != nullptr) {
+    char* base = reinterpret_cast<char*>(out->part_o);
+    out->part_ml = reinterpret_cast<float2*>(base + ml);
+    out->notes = reinterpret_cast<JoinNote*>(base + notes);
+  }
+  return notes + align_up(static_cast<size_t>(p.ctas) * sizeof(JoinNote));
+}
+
 // Everything of a call that does not depend on its tensors: sizes, the kernel's tiles and splits,
 // and the workspace.
 ba_status plan(const ba_kv_cache* cache, const ba_paged_seqs* s, PagedAttnParams* p, size_t* ws) {
@@ -81,14 +93,20 @@ ba_status plan(const ba_kv_cache* cache, const ba_paged_seqs* s, PagedAttnParams
   const int64_t tiles = ceil_div(rows, p->row_tile);
   if (tiles > kMaxCtas / (static_cast<int64_t>(p->B) * p->cache.heads)) return BA_ERR_UNSUPPORTED;
   p->row_tiles = static_cast<int>(tiles);
-  int blocks = 0;
-  p->split_blocks = p->row_tile == 256 ? paged_chunk_split_blocks(*p, sm_count(), &blocks)
-                                       : paged_decode_split_blocks(*p, sm_count(), &blocks);
-  p->nsplit = std::max(1, static_cast<int>(ceil_div(blocks, p->split_blocks)));
-  if (tiles * p->B * p->cache.heads > kMaxCtas / std::max(p->nsplit, p->row_tile)) return BA_ERR_UNSUPPORTED;
-  if (p->nsplit > 1) {
-    const size_t n = static_cast<size_t>(p->nsplit) * p->T * p->heads;
-    *ws = align_up(n * p->cache.dp * 4) + align_up(n * 8);
+  if (tiles * p->B * p->cache.heads > kMaxCtas / p->row_tile) return BA_ERR_UNSUPPORTED;
+  p->nsplit = 1;
+  if (p->row_tile == 256) {
+    int blocks = 0;
+    p->split_blocks = paged_chunk_split_blocks(*p, sm_count(), &blocks);
+    p->nsplit = std::max(1, static_cast<int>(ceil_div(blocks, p->split_blocks)));
+    if (tiles * p->B * p->cache.heads > kMaxCtas / p->nsplit) return BA_ERR_UNSUPPORTED;
+    if (p->nsplit > 1) {
+      const size_t n = static_cast<size_t>(p->nsplit) * p->T * p->heads;
+      *ws = align_up(n * p->cache.dp * 4) + align_up(n * 8);
+    }
+  } else {
+    p->ctas = paged_decode_ctas(*p, sm_count());
+    if (p->ctas > 0) *ws = line_workspace(*p, nullptr);
   }
   return BA_OK;
 }
@@ -171,7 +189,10 @@ ba_status ba_attention_paged(const void* q, int64_t q_stride_t, int64_t q_stride
     if (!aligned(ws, 16)) return BA_ERR_ALIGNMENT;
     p.part_o = static_cast<float*>(ws);
     const size_t n = static_cast<size_t>(p.nsplit) * p.T * p.heads;
-    p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + align_up(n * p.cache.dp * 4));
+    if (p.ctas > 0)
+      line_workspace(p, &p);
+    else
+      p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + align_up(n * p.cache.dp * 4));
   }
   p.q = q;
   p.q_stride_t = q_stride_t;

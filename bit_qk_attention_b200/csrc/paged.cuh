@@ -41,6 +41,7 @@ struct CacheReadParams {
 };
 
 // Attention of new tokens over the cache.
+struct JoinNote;
 struct PagedAttnParams {
   CacheView cache;
   const void* q;
@@ -63,6 +64,8 @@ struct PagedAttnParams {
   int row_tiles;   // tiles of a sequence and KV head (most)
   float* part_o;   // [nsplit][T * heads][dp] unnormalised sums, when nsplit > 1
   float2* part_ml; // [nsplit][T * heads] (maximum in log2, sum)
+  int ctas;          // CTAs that share the line of units; 0: one CTA per (tile, head), nothing is cut
+  JoinNote* notes;   // [ctas]
 };
 
 // What a CTA works on: a tile of rows r = i * group + g (i-th new token, g-th head of the group) of
@@ -104,6 +107,76 @@ __device__ __forceinline__ RowTile row_tile(const PagedAttnParams& p, int b, int
   return w;
 }
 
+// The work of a launch is a line of units, for all sequences' row tiles, one KV head after the other:
+// `cost` units that stand for starting and ending a (tile, head), then one for each of its key blocks.
+// Each CTA takes the same number of units, whatever the lengths are, so the blocks of a (tile, head)
+// may be cut at the ends of CTAs. What a CTA computes of a cut one goes into the workspace: slot 0 if
+// it began before the CTA, else slot 1. The CTA in which a cut one begins leaves a note for the
+// kernel that joins the parts.
+struct JoinNote {
+  int entry, head;  // entry = b * row_tiles + tile
+  int last;         // CTA with the last part; the CTAs between have it in slot 0. -1: nothing to join
+};
+
+__device__ __forceinline__ RowTile entry_tile(const PagedAttnParams& p, int entry, int bk) {
+  const int b = entry / p.row_tiles;
+  return row_tile(p, b, entry - b * p.row_tiles, bk);
+}
+
+__device__ __forceinline__ int units_of(const RowTile& w, int cost) { return w.rows > 0 ? cost + w.nblk : 0; }
+
+// A CTA's stretch [at, end) of the line, `per` units or fewer; `at` lies in `entry`, whose units
+// start at `base`.
+struct Stretch {
+  int64_t at, end, base;
+  int per, entry;
+};
+
+template <int THREADS>
+__device__ __forceinline__ Stretch find_stretch(const PagedAttnParams& p, int bk, int cost, int min_units) {
+  __shared__ int64_t s_warp[THREADS / 32], s_base;
+  __shared__ int s_entry;
+  const int heads = p.cache.heads, n = p.B * p.row_tiles, each = (n + THREADS - 1) / THREADS;
+  const int i0 = min(n, static_cast<int>(threadIdx.x) * each), i1 = min(n, i0 + each);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t sum = 0;
+  for (int i = i0; i < i1; ++i) sum += units_of(entry_tile(p, i, bk), cost);
+  int64_t upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) s_warp[warp] = upto;
+  __syncthreads();
+  int64_t total = 0, before = upto - sum;
+#pragma unroll
+  for (int k = 0; k < THREADS / 32; ++k) {
+    if (k < warp) before += s_warp[k];
+    total += s_warp[k];
+  }
+  total *= heads;
+  Stretch st;
+  st.per = static_cast<int>(max(ceil_div(total, gridDim.x), static_cast<int64_t>(min_units)));
+  st.at = static_cast<int64_t>(blockIdx.x) * st.per;
+  st.end = min(total, st.at + st.per);
+  int64_t base = before * heads;
+  if (st.at < st.end && base <= st.at && st.at < base + sum * heads) {
+    int i = i0;
+    for (;; ++i) {
+      const int64_t u = static_cast<int64_t>(units_of(entry_tile(p, i, bk), cost)) * heads;
+      if (st.at < base + u) break;
+      base += u;
+    }
+    s_entry = i;
+    s_base = base;
+  }
+  __syncthreads();
+  st.entry = s_entry;
+  st.base = s_base;
+  return st;
+}
+
 // Parts of the key axis that a tile of nblk blocks uses.
 __device__ __forceinline__ int splits_used(const PagedAttnParams& p, int nblk) {
   return max(1, min(p.nsplit, static_cast<int>(ceil_div(nblk, p.split_blocks))));
@@ -140,6 +213,9 @@ __device__ __forceinline__ void cta_of(const PagedAttnParams& p, unsigned idx, i
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -162,8 +238,8 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 
 cudaError_t launch_paged_decode(const PagedAttnParams& p, int dt, cudaStream_t s);
 cudaError_t launch_paged_chunk(const PagedAttnParams& p, int dt, cudaStream_t s);
-// Key blocks of a part on a device of `sms` SMs, and the most blocks that a tile can have.
-int paged_decode_split_blocks(const PagedAttnParams& p, int sms, int* max_blocks);
+// CTAs that share the work on a device of `sms` SMs (0: one CTA per tile and head).
+int paged_decode_ctas(const PagedAttnParams& p, int sms);
 int paged_chunk_split_blocks(const PagedAttnParams& p, int sms, int* max_blocks);
 // Second kernel of a split launch: joins the parts of the row tiles (key blocks of bk tokens).
 cudaError_t launch_paged_join(const PagedAttnParams& p, int bk, cudaStream_t s);

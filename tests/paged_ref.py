@@ -56,6 +56,8 @@ def attend(q, block, ps, d, table, kv_lens, cu, causal=True, window=0, sinks=0, 
     exponent: scores are a few fp32 products of at most max|s|, together within 2^-19 (1 + max|s|). Weights below
     fp16's normal range are off by at most 2^-25 of the largest weight's unit, times a code of at most 127 in the
     largest exponent. The product adds n / 16 partial sums in fp32. The output rounds once.
+    With few rows the weights are fixed-point numbers instead, in units of 1 / 65280 of the largest w_j 2^e_j of a
+    block: each of the n weights is off by at most half a unit, times a code of at most 127.
     """
     codes, _, neg, mu, ex = split_block(block, ps, d)
     P, Hkv = block.shape[:2]
@@ -94,6 +96,7 @@ def attend(q, block, ps, d, table, kv_lens, cu, causal=True, window=0, sinks=0, 
                 up = 2.0 ** int(e[see, h // G].max())
                 A = w @ vv.abs()
                 to[t0 + i, h] = A * (2.0 ** -11 + 2.0 ** -18 * (1 + big) + (m / 16) * 2.0 ** -23) \
-                    + m * 2.0 ** -25 * 127 * up + o[t0 + i, h].abs() * eps_out / 2 * (1 + 2.0 ** -10)
+                    + m * 2.0 ** -25 * 127 * up \
+                    + m * 127 * 0.5 / 65280 * float((w * 2.0 ** e[see, h // G].to(F64)).max()) + o[t0 + i, h].abs() * eps_out / 2 * (1 + 2.0 ** -10)
                 tl[t0 + i, h] = 2.0 ** -19 * (1 + big) + m * 2.0 ** -26
     return o, lse, to, tl
