@@ -330,16 +330,16 @@ def kv_block_bytes(page_size: int, d: int) -> int:
     return lib().ba_kv_block_bytes(page_size, d)
 
 
-@dataclass
 class KVCache:
     """A paged cache of binary K and 8-bit V rows (layout: include/binattn.h, ba_kv_cache).
 
     data: uint8 CUDA tensor [num_pages, n_kv_heads, kv_block_bytes(page_size, d)], contiguous.
     ``KVCache.zeros`` allocates one; any slice of a larger buffer of that shape does as well.
     """
-    data: object
-    page_size: int
-    d: int
+
+    def __init__(self, data, page_size: int, d: int):
+        self._data, self._page_size, self._d = data, page_size, d
+        self._c = None  # the C description, checked when it is first asked for
 
     @classmethod
     def zeros(cls, num_pages: int, n_kv_heads: int, d: int, page_size: int = 64, device="cuda") -> "KVCache":
@@ -350,108 +350,117 @@ class KVCache:
         return cls(torch.zeros((num_pages, n_kv_heads, nbytes), dtype=torch.uint8, device=device), page_size, d)
 
     @property
+    def data(self):
+        return self._data
+
+    @property
+    def page_size(self) -> int:
+        return self._page_size
+
+    @property
+    def d(self) -> int:
+        return self._d
+
+    @property
     def num_pages(self) -> int:
-        return self.data.shape[0]
+        return self._data.shape[0]
 
     @property
     def n_kv_heads(self) -> int:
-        return self.data.shape[1]
+        return self._data.shape[1]
 
     def _part(self, at: int, width: int):
-        return self.data[:, :, self.page_size * at:self.page_size * (at + width)]
+        return self._data[:, :, self._page_size * at:self._page_size * (at + width)]
 
     @property
     def v_codes(self):
         """int8 codes of V [num_pages, n_kv_heads, page_size, v_row_bytes(d)] (a view)."""
-        dp = v_row_bytes(self.d)
-        return self._part(0, dp).view(_torch().int8).unflatten(2, (self.page_size, dp))
+        dp = v_row_bytes(self._d)
+        return self._part(0, dp).view(_torch().int8).unflatten(2, (self._page_size, dp))
 
     @property
     def k_bits(self):
         """Sign words of K, int32 [num_pages, n_kv_heads, page_size, 4] (a view)."""
-        return self._part(v_row_bytes(self.d), 16).view(_torch().int32).unflatten(2, (self.page_size, 4))
+        return self._part(v_row_bytes(self._d), 16).view(_torch().int32).unflatten(2, (self._page_size, 4))
 
     @property
     def k_mu(self):
         """bf16 scales of K [num_pages, n_kv_heads, page_size] (a view)."""
-        return self._part(v_row_bytes(self.d) + 16, 2).view(_torch().bfloat16)
+        return self._part(v_row_bytes(self._d) + 16, 2).view(_torch().bfloat16)
 
     @property
     def v_exp(self):
         """int8 exponents of V [num_pages, n_kv_heads, page_size] (a view)."""
-        return self._part(v_row_bytes(self.d) + 18, 1).view(_torch().int8)
+        return self._part(v_row_bytes(self._d) + 18, 1).view(_torch().int8)
 
     def c(self) -> CKvCache:
-        torch = _torch()
-        t = self.data
-        if t.dtype != torch.uint8 or t.dim() != 3 or not t.is_cuda or not t.is_contiguous():
-            raise ValueError("cache data must be a contiguous uint8 CUDA tensor [pages, heads, block bytes]")
-        if t.shape[2] != kv_block_bytes(self.page_size, self.d) or t.shape[2] == 0:
-            raise ValueError("cache blocks must have kv_block_bytes(page_size, d) bytes")
-        return CKvCache(t.data_ptr(), t.shape[0], self.page_size, t.shape[1], self.d)
+        t = self._data
+        if self._c is None:
+            if t.dtype != _torch().uint8 or t.dim() != 3 or not t.is_cuda or not t.is_contiguous():
+                raise ValueError("cache data must be a contiguous uint8 CUDA tensor [pages, heads, block bytes]")
+            if t.shape[2] != kv_block_bytes(self._page_size, self._d) or t.shape[2] == 0:
+                raise ValueError("cache blocks must have kv_block_bytes(page_size, d) bytes")
+            self._c = CKvCache(t.data_ptr(), t.shape[0], self._page_size, t.shape[1], self._d)
+        return self._c
 
 
-class _On:
-    """Makes a tensor's device current, and a given stream too, so that what torch allocates inside
-    belongs to the stream the kernels run on; `stream` is then that stream's handle."""
-
-    def __init__(self, t, stream):
-        torch = _torch()
-        self.ctx = None
-        if stream is not None:
-            if stream.device != t.device:
-                raise ValueError("stream and tensors must be on one device")
-            self.ctx = torch.cuda.stream(stream)
-        elif t.device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(t.device)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return _stream()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+# The entry points below run many times per second on small tensors, so their checks are written for
+# little Python. What they allocate, and their kernels, belong to the current stream of the cache's
+# device; a call for another stream, or from another current device, is made again inside of it.
+def _elsewhere(dev: int, stream) -> bool:
+    return stream is not None or dev != _torch()._C._cuda_getDevice()
 
 
-def _same_device(ref, **ts):
-    for name, t in ts.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} must be on the cache's device")
+def _on(cache, stream):
+    torch = _torch()
+    if stream is None:
+        return torch.cuda.device(cache.data.device)
+    if stream.device != cache.data.device:
+        raise ValueError("stream and cache must be on one device")
+    return torch.cuda.stream(stream)
 
 
-def _index_check(t, name: str, dtype, shape=None):
-    if t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}")
+def _check_index(t, name: str, dtype, dev: int, shape):
+    if t.dtype != dtype or t.get_device() != dev or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on the cache's device")
 
 
-def _rows_check(t, name: str, heads, d: int):
+def _check_rows(t, name: str, dev: int, heads, d: int) -> int:
+    """Checks rows [tokens, heads, d] of 16-bit numbers; returns their ba_dtype."""
     torch = _torch()
     if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
         raise ValueError(f"{name} must be [tokens, heads, {d}] with the cache's heads")
-    if t.dtype not in (torch.float16, torch.bfloat16):
-        raise ValueError(f"{name} must be fp16 or bf16")
     if t.stride(2) != 1 and d > 1 and t.numel() > 0:
         raise ValueError(f"{name} must be contiguous in its last dimension")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the cache's device")
+    dt = t.dtype
+    if dt == torch.bfloat16:
+        return BA_BF16
+    if dt == torch.float16:
+        return BA_F16
+    raise ValueError(f"{name} must be fp16 or bf16")
 
 
 def cache_write(cache: KVCache, k, v, slots, stream=None) -> None:
     """Quantise new rows k, v [T, n_kv_heads, d] (fp16/bf16; strided views are taken as they are)
     and write them to the tokens at slots (int64 [T], page * page_size + offset; -1 skips a row).
     Slots in range must differ."""
+    torch = _torch()
     cc = cache.c()
-    _rows_check(k, "k", cc.n_kv_heads, cache.d)
-    _rows_check(v, "v", cc.n_kv_heads, cache.d)
-    if k.shape != v.shape or k.dtype != v.dtype:
+    dev = cache.data.get_device()
+    if _elsewhere(dev, stream):
+        with _on(cache, stream):
+            return cache_write(cache, k, v, slots)
+    dt = _check_rows(k, "k", dev, cc.n_kv_heads, cc.d)
+    if _check_rows(v, "v", dev, cc.n_kv_heads, cc.d) != dt or v.shape[0] != k.shape[0]:
         raise ValueError("k and v must share dtype and shape")
-    _same_device(cache.data, k=k, v=v, slots=slots)
-    _index_check(slots, "slots", _torch().int64, (k.shape[0],))
-    with _On(cache.data, stream) as s:
-        _check(lib().ba_cache_write(_ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1), _dt(k),
-                                    k.shape[0], _ptr(slots), ctypes.byref(cc), s), "ba_cache_write")
+    T = k.shape[0]
+    _check_index(slots, "slots", torch.int64, dev, (T,))
+    kt, kh, _ = k.stride()
+    vt, vh, _ = v.stride()
+    _check(lib().ba_cache_write(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, dt, T, slots.data_ptr(),
+                                ctypes.byref(cc), torch._C._cuda_getCurrentRawStream(dev)), "ba_cache_write")
 
 
 def cache_read(cache: KVCache, slots, dtype=None, k_out=None, v_out=None, stream=None) -> Tuple[object, object]:
@@ -459,39 +468,23 @@ def cache_read(cache: KVCache, slots, dtype=None, k_out=None, v_out=None, stream
     dtype: fp16, bf16 (default) or fp32, or that of k_out / v_out where they are given."""
     torch = _torch()
     cc = cache.c()
-    _same_device(cache.data, slots=slots, k_out=k_out, v_out=v_out)
-    _index_check(slots, "slots", torch.int64, (slots.numel(),))
-    shape = (slots.numel(), cc.n_kv_heads, cache.d)
+    dev = cache.data.get_device()
+    if _elsewhere(dev, stream):
+        with _on(cache, stream):
+            return cache_read(cache, slots, dtype, k_out, v_out)
+    T = slots.numel()
+    _check_index(slots, "slots", torch.int64, dev, (T,))
+    shape = (T, cc.n_kv_heads, cc.d)
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is not None:
             dtype = dtype or t.dtype
-            _index_check(t, name, dtype, shape)
+            _check_index(t, name, dtype, dev, shape)
     dtype = dtype or torch.bfloat16
-    with _On(cache.data, stream) as s:
-        k = torch.empty(shape, dtype=dtype, device=slots.device) if k_out is None else k_out
-        v = torch.empty(shape, dtype=dtype, device=slots.device) if v_out is None else v_out
-        _check(lib().ba_cache_read(ctypes.byref(cc), _ptr(slots), shape[0], _ptr(k), _ptr(v), _dt(k), s),
-               "ba_cache_read")
+    k = slots.new_empty(shape, dtype=dtype) if k_out is None else k_out
+    v = torch.empty_like(k) if v_out is None else v_out
+    _check(lib().ba_cache_read(ctypes.byref(cc), slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), _dt(k),
+                               torch._C._cuda_getCurrentRawStream(dev)), "ba_cache_read")
     return k, v
-
-
-def _paged_seqs(q, cc, page_size, page_table, kv_lens, cu_seqlens_q, max_q_len, max_kv_len, causal, window, sinks):
-    torch = _torch()
-    B = kv_lens.numel()
-    _index_check(kv_lens, "kv_lens", torch.int32, (B,))
-    if cu_seqlens_q is not None:
-        _index_check(cu_seqlens_q, "cu_seqlens_q", torch.int32, (B + 1,))
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B or \
-            (page_table.stride(1) != 1 and page_table.shape[1] > 1):
-        raise ValueError("page_table must be an int32 tensor [sequences, pages], contiguous in its last dimension")
-    pages = page_table.shape[1]
-    if max_q_len is None:
-        max_q_len = 1 if cu_seqlens_q is None else q.shape[0]
-    if max_kv_len is None:
-        max_kv_len = pages * page_size
-    return CPagedSeqs(B, q.shape[0], q.shape[1], max_q_len, max_kv_len,
-                      0 if cu_seqlens_q is None else cu_seqlens_q.data_ptr(), kv_lens.data_ptr(),
-                      page_table.data_ptr(), page_table.stride(0), pages, 1 if causal else 0, window, sinks)
 
 
 def attention_paged(q, cache: KVCache, page_table, kv_lens, cu_seqlens_q=None, max_q_len: Optional[int] = None,
@@ -507,31 +500,58 @@ def attention_paged(q, cache: KVCache, page_table, kv_lens, cu_seqlens_q=None, m
     max_q_len, max_kv_len: host bounds of the lengths (defaults: T, and the page table's tokens).
                   Tight bounds let the launch be chosen well; lengths are read on the device.
     window:       > 0: a token sees itself and the window - 1 tokens before it, and the first `sinks`.
+    workspace:    uint8 CUDA tensor of at least the bytes that ba_paged_workspace_bytes tells
+                  (default: allocated for the call). Calls that can overlap need one each.
     Returns o [T, n_heads, d] (out_dtype, default q's; rows of no sequence are left as they were in
     `out`), and with return_lse also the fp32 log of the softmax sums [T, n_heads].
     """
     torch = _torch()
     cc = cache.c()
-    _rows_check(q, "q", None, cache.d)
-    _same_device(cache.data, q=q, page_table=page_table, kv_lens=kv_lens, cu_seqlens_q=cu_seqlens_q, out=out,
-                 workspace=workspace)
-    sq = _paged_seqs(q, cc, cache.page_size, page_table, kv_lens, cu_seqlens_q, max_q_len, max_kv_len, causal,
-                     window, sinks)
+    dev = cache.data.get_device()
+    if _elsewhere(dev, stream):
+        with _on(cache, stream):
+            return attention_paged(q, cache, page_table, kv_lens, cu_seqlens_q, max_q_len, max_kv_len, causal, window,
+                                   sinks, softmax_scale, out, out_dtype, return_lse, workspace)
+    dt = _check_rows(q, "q", dev, None, cc.d)
+    T, heads, _ = q.shape
+    B = kv_lens.numel()
+    _check_index(kv_lens, "kv_lens", torch.int32, dev, (B,))
+    cu = 0
+    if cu_seqlens_q is not None:
+        _check_index(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev, (B + 1,))
+        cu = cu_seqlens_q.data_ptr()
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B or \
+            (page_table.stride(1) != 1 and page_table.shape[1] > 1) or page_table.get_device() != dev:
+        raise ValueError("page_table must be an int32 tensor [sequences, pages] on the cache's device, contiguous in "
+                         "its last dimension")
+    pages = page_table.shape[1]
+    if max_q_len is None:
+        max_q_len = 1 if cu_seqlens_q is None else T
+    if max_kv_len is None:
+        max_kv_len = pages * cc.page_size
     if out is not None:
-        _index_check(out, "out", out_dtype or out.dtype, tuple(q.shape))
-    with _On(cache.data, stream) as s:
-        if out is None:
-            out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
-        nws = lib().ba_paged_workspace_bytes(ctypes.byref(cc), ctypes.byref(sq))
-        if nws == ctypes.c_size_t(-1).value:  # unsupported: the call below reports it
-            nws = 0
-        if workspace is None:
-            workspace = torch.empty(nws, dtype=torch.uint8, device=q.device) if nws else None
-        _check(lib().ba_attention_paged(_ptr(q), q.stride(0), q.stride(1), _dt(q), ctypes.byref(cc),
-                                        ctypes.byref(sq), float(softmax_scale), _ptr(out), _dt(out), _ptr(lse),
-                                        _ptr(workspace), 0 if workspace is None else workspace.numel(), s),
-               "ba_attention_paged")
+        _check_index(out, "out", out_dtype or out.dtype, dev, (T, heads, cc.d))
+        odt = _dt(out)
+    else:
+        out = torch.empty_like(q, dtype=out_dtype, memory_format=torch.contiguous_format)
+        odt = dt if out_dtype is None else _dt(out)
+    lse = q.new_empty((T, heads), dtype=torch.float32) if return_lse else None
+    L = lib()
+    sq = CPagedSeqs(B, T, heads, max_q_len, max_kv_len, cu, kv_lens.data_ptr(), page_table.data_ptr(),
+                    page_table.stride(0), pages, 1 if causal else 0, window, sinks)
+    c_cache, c_seqs = ctypes.byref(cc), ctypes.byref(sq)
+    nws = L.ba_paged_workspace_bytes(c_cache, c_seqs)
+    if workspace is None:
+        # (size_t) -1 stands for arguments that the call below refuses.
+        if 0 < nws != ctypes.c_size_t(-1).value:
+            workspace = kv_lens.new_empty((nws,), dtype=torch.uint8)
+    elif workspace.get_device() != dev:
+        raise ValueError("workspace must be on the cache's device")
+    qt, qh, _ = q.stride()
+    _check(L.ba_attention_paged(q.data_ptr(), qt, qh, dt, c_cache, c_seqs, softmax_scale, out.data_ptr(), odt,
+                                0 if lse is None else lse.data_ptr(), 0 if workspace is None else workspace.data_ptr(),
+                                0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                torch._C._cuda_getCurrentRawStream(dev)), "ba_attention_paged")
     return (out, lse) if return_lse else out
 
 

@@ -1,6 +1,7 @@
 // C-ABI layer of the paged cache: argument checks and launches. The entry points are declared and
 // documented in include/binattn.h.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -38,13 +39,17 @@ ba_status check_cache(const ba_kv_cache* c, CacheView* out) {
 }
 
 int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();  // no device here: the workspace query still answers
-    return 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) {
+    if (dev < 64 && (sms = known[dev].load()) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) {
+      if (dev < 64) known[dev].store(sms);
+      return sms;
+    }
   }
-  return sms;
+  cudaGetLastError();  // no device here: the workspace query still answers
+  return 148;
 }
 
 size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -74,6 +79,7 @@ ba_status plan(const ba_kv_cache* cache, const ba_paged_seqs* s, PagedAttnParams
   if (s->window > 0 && s->causal != 1) return BA_ERR_INVALID_ARG;
   if (s->n_heads % cache->n_kv_heads != 0) return BA_ERR_INVALID_ARG;
   if (s->max_kv_len > kMaxKv || s->T > kMaxRows / s->n_heads) return BA_ERR_UNSUPPORTED;
+  if (cache->num_pages > ((int64_t{1} << 31) - 1) / cache->n_kv_heads) return BA_ERR_UNSUPPORTED;
   p->B = s->B;
   p->heads = s->n_heads;
   p->group = s->n_heads / cache->n_kv_heads;

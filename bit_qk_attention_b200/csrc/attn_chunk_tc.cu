@@ -31,7 +31,7 @@
 
 namespace binattn {
 
-__device__ int g_paged_status = 0;
+__device__ int g_chunk_status = 0;
 
 namespace {
 
@@ -82,7 +82,7 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
     if (yield && *abort_flag) return false;
     if (globaltimer() - t0 > kTimeoutNs) {
       *abort_flag = 1;
-      atomicExch(&g_paged_status, 1);
+      atomicExch(&g_chunk_status, 1);
       return false;
     }
   }
@@ -502,15 +502,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
 
 template <int CH>
 cudaError_t launch_chunk(const PagedAttnParams& p, int dt, cudaStream_t s) {
-  auto kernel = paged_chunk_kernel<CH>;
   // At least half of the shared memory: the CTA owns all of the SM's tensor memory.
   const int smem = std::max(Cfg<CH>::kBytes, 116 * 1024);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem<paged_chunk_kernel<CH>>(smem);
   if (e != cudaSuccess) return e;
   const bool wide = p.cache.d % 8 == 0 && reinterpret_cast<uintptr_t>(p.q) % 16 == 0 &&
                     (p.q_stride_t | p.q_stride_h) % 8 == 0;
   const int64_t grid = static_cast<int64_t>(p.B) * p.row_tiles * p.cache.heads * p.nsplit;
-  kernel<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(p, dt == BA_F16 ? 1 : 0, wide ? 1 : 0);
+  paged_chunk_kernel<CH><<<static_cast<unsigned>(grid), kThreads, smem, s>>>(p, dt == BA_F16 ? 1 : 0, wide ? 1 : 0);
   if ((e = cudaGetLastError()) != cudaSuccess || p.nsplit == 1) return e;
   return launch_paged_join(p, kBlk, s);
 }
@@ -531,14 +530,8 @@ int paged_chunk_split_blocks(const PagedAttnParams& p, int sms, int* max_blocks)
   return static_cast<int>(std::max<int64_t>(1, ceil_div(blocks, parts)));
 }
 
-cudaError_t read_and_clear_paged_status(int* value, cudaStream_t s) {
-  cudaError_t e = cudaMemcpyFromSymbolAsync(value, g_paged_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
-  if (e != cudaSuccess) return e;
-  if ((e = cudaStreamSynchronize(s)) != cudaSuccess) return e;
-  const int zero = 0;
-  if ((e = cudaMemcpyToSymbolAsync(g_paged_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s)) != cudaSuccess)
-    return e;
-  return cudaStreamSynchronize(s);
+cudaError_t read_and_clear_chunk_status(int* value, cudaStream_t s) {
+  return read_and_clear_status(g_chunk_status, value, s);
 }
 
 }  // namespace binattn

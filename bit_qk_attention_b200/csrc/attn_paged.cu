@@ -5,7 +5,8 @@
 // is kept small:
 //   * A CTA takes one sequence, one KV head, up to 8 NR rows (new tokens x heads of the group, which
 //     share every key) and a part of the key axis. Each of its warps walks 32-key blocks of its own
-//     through a ring of cp.async stages, with no synchronisation between warps until the end.
+//     through a ring of TMA stages (V through a tensor map whose swizzle keeps ldmatrix free of bank
+//     conflicts, the rest as plain bulk copies), with no synchronisation between warps until the end.
 //   * Scores are products of whole numbers on the tensor cores (mma.sync m16n8k32, int8). With K's
 //     sign bits k in {0, 1} and Q in {-1, +1}, x = sum q - 2 sum q k. The bits need no expanding: a
 //     word masked by 0x01010101 << s holds four of them as bytes of value 2^s, and the byte of Q that
@@ -18,7 +19,8 @@
 //     making fp16 numbers of them took more instructions than all the rest. The weights of a block
 //     are 16-bit fixed-point numbers, round(65280 2^(s - m)) with m the row's maximum in the block:
 //     a product each for their high and low bytes, whose exact sums are weighted by 2^(m - M) and
-//     added in fp32. A weight's error is 2^-17 of the block's largest.
+//     added in fp32. A weight's error is 2^-17 of the block's largest. Scores come out by key and
+//     weights go in by row; movmatrix turns them, as 16-bit numbers, in between.
 //   * A value row's exponent e_j joins the score instead of the codes: the weight is
 //     2^(s_j + e_j - m) with m a maximum of s_j + e_j, and the softmax sum adds weight * 2^-e_j. The
 //     reference M moves (and the sums are rescaled) only when a block's m passes it by 2^40, far
@@ -32,10 +34,16 @@
 
 #include "kernels.h"
 #include "paged.cuh"
+#include "tc_ptx.cuh"
+#include "tensormap.h"
 
 namespace binattn {
 
+__device__ int g_decode_status = 0;
+
 namespace {
+
+using namespace ptx;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
@@ -47,11 +55,7 @@ constexpr float kUnit = 65280.0f;  // weight 1 in fixed point: 255 * 256
 constexpr int kMagicBits = 0x4B400000;  // 1.5 * 2^23
 constexpr float kMagic = 12582912.0f;
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
+__device__ __forceinline__ float ex2(float x) { return ex2_approx(x); }
 
 __device__ __forceinline__ float4 lds_f4(uint32_t a) {
   const uint4 u = lds128(a);
@@ -62,21 +66,26 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
-__device__ __forceinline__ void sts_f32(uint32_t a, float x) {
-  asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
-}
 
-// c += A B: A 16 x 32 signed bytes (rows g and g + 8 of Q), B 32 x 8 unsigned bytes (keys' bits).
-__device__ __forceinline__ void mma_i8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+// c (+)= A B: A 16 x 32 unsigned bytes (keys g and g + 8), B 32 x 8 signed bytes (rows of Q).
+__device__ __forceinline__ void mma_qk_first(int (&c)[4], const int (&start)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(start[0]), "r"(start[1]), "r"(start[2]),
+        "r"(start[3]));
+}
+__device__ __forceinline__ void mma_qk(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// c = start + A B.
-__device__ __forceinline__ void mma_i8_first(int (&c)[4], const int (&start)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+// c = start + A B: A 16 channels x 32 keys of signed codes, B 32 keys x 8 rows of unsigned bytes.
+__device__ __forceinline__ void mma_pv(int (&c)[4], const int (&start)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                              uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
@@ -93,28 +102,54 @@ __device__ __forceinline__ void ldmatrix_t8(uint32_t a, uint32_t (&r)[4]) {
                : "r"(a));
 }
 
+// 8 x 8 matrix of 16-bit numbers, transposed: the lane (g, t) gives row g, columns 2 t and 2 t + 1.
+__device__ __forceinline__ uint32_t turn8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // Whole-number results (kMagicBits + n, |n| < 2^22) as floats n.
 __device__ __forceinline__ float2 whole(int x, int y) {
   return __fadd2_rn(make_float2(__int_as_float(x), __int_as_float(y)), make_float2(-kMagic, -kMagic));
 }
 
-// Shared memory of a warp: V rows of kRow bytes for each stage (16-byte pieces permuted), then each
-// stage's sign rows, mu and exponents. Once a block's sign rows are read, what its scores need per
-// key as floats (mu, e, 2^-e) takes their place. Four CTAs of four warps just fit an SM.
+// Shared memory of a warp: V rows of kRow bytes for each stage as the tensor map's swizzle leaves
+// them, then each stage's sign rows, mu and exponents. Once a block's sign rows are read, what its
+// scores need per key as floats (mu, e, 2^-e) takes their place. Four CTAs of four warps just fit an SM.
 template <int CPG>  // eighths of the channels: 16 (rows of 128 bytes) or 8 (rows of 64)
 struct Ring {
   static constexpr int kRow = CPG * 8;
   static constexpr int kV = kBlk * kRow;
   static constexpr int offX = kStages * kV;
   static constexpr int xMu = kBlk * 16, xExp = xMu + kBlk * 2, kX = xExp + kBlk;
-  static constexpr int kBytes = offX + kStages * kX;
-  static_assert(3 * kBlk * 4 <= xMu, "the floats replace the sign rows");
-  // Byte offset of the 16-byte piece c of key j: eight neighbouring keys' pieces c lie in
-  // different banks.
+  static constexpr int kBytes = offX + kStages * kX;  // of a warp
+  // Behind the warps' rings: barriers, sums of the warps, sign words and scales of the rows, scratch.
+  static constexpr int offFull = kWarps * kBytes;
+  static constexpr int offMl = offFull + kWarps * kStages * 8;
+  static __host__ __device__ constexpr int offBits(int rows) { return offMl + kWarps * rows * 8; }
+  static __host__ __device__ constexpr int offMu(int rows) { return offBits(rows) + rows * 16; }
+  static __host__ __device__ constexpr int offScratch(int rows) { return offMu(rows) + rows * 4; }
+  static __host__ __device__ constexpr int total(int rows) { return offScratch(rows) + (kWarps + 2) * 8; }
+  static constexpr int kHalf = kPageUnit * (kRow + 16 + 2 + 1);  // bytes that 16 tokens bring
+  // Byte offset of the 16-byte piece c of key j: the swizzle of 128- or 64-byte rows.
   static __device__ __forceinline__ int piece(int j, int c) {
     return kRow == 128 ? (j * 8 + (c ^ (j & 7))) * 16 : (j * 4 + (c ^ ((j >> 1) & 3))) * 16;
   }
 };
+
+// Waits, a second at most, for a stage's copies; records a timeout.
+__device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity)) {
+    if (globaltimer() - t0 > 1000000000ull) {
+      atomicExch(&g_decode_status, 1);
+      return false;
+    }
+  }
+  return true;
+}
 
 // One row of q by a warp: sign words and sum of |x|.
 template <typename T>
@@ -130,26 +165,38 @@ __device__ __forceinline__ void scan_row(const T* src, int d, int lane, uint32_t
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
 }
 
-template <int CPG, int NR, bool FULL>  // FULL: dp is the whole CPG * 8
-__global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 3) paged_decode_kernel(PagedAttnParams p, int q_f16) {
+template <int CPG, int NR>
+__global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 3)
+    paged_decode_kernel(PagedAttnParams p, int q_f16, const __grid_constant__ CUtensorMap v_map) {
   using S = Ring<CPG>;
   constexpr int MT = CPG / 2;  // 16-channel tiles
   constexpr int R = 8 * NR;    // rows of a CTA
   constexpr int CH = CPG * 8;  // channels of the accumulators (>= d)
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint32_t s_bits[R][4];
-  __shared__ float s_mu[R];
-  __shared__ float2 s_ml[kWarps][R];
+  extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int oBits = S::offBits(R), oMu = S::offMu(R), oScratch = S::offScratch(R);
+  auto s_full = reinterpret_cast<uint64_t(*)[kStages]>(smem + S::offFull);
+  auto s_ml = reinterpret_cast<float2(*)[R]>(smem + S::offMl);
+  auto s_bits = reinterpret_cast<uint32_t(*)[4]>(smem + oBits);
+  auto s_mu = reinterpret_cast<float*>(smem + oMu);
 
   allow_dependents();
   const CacheView& cv = p.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  // The V stages of all warps come first (they start on 128 bytes).
-  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+  const int dp = cv.dp;
+  // The V stages of all warps come first (they start on 1024 bytes, where the swizzle starts).
+  const uint32_t base = smem_u32(smem);
   const uint32_t vring = base + warp * S::offX, xring = base + kWarps * S::offX + warp * kStages * S::kX;
+  if (lane < kStages) {
+    mbar_init(&s_full[warp][lane], 1);
+    mbar_fence_init();
+  }
+  __syncwarp();
+  int st = 0;          // stage of the next block, and the parity of its next arrival
+  uint32_t phase = 0;
+  bool ok = true;
   Stretch line{};
   if (p.ctas > 0) {
-    line = find_stretch<kThreads>(p, kBlk, kCost, kWarps);
+    line = find_stretch<kThreads>(p, kBlk, kCost, kWarps, reinterpret_cast<int64_t*>(smem + oScratch));
     if (line.at >= line.end) {
       if (threadIdx.x == 0) p.notes[blockIdx.x].last = -1;
       return;
@@ -195,61 +242,46 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 3) paged_decode_kernel
 
   // The warp's blocks are v0 + warp, v0 + warp + kWarps, ... Lane l keeps the page and the offset
   // in it of the 16 tokens (l % 2) of the block l / 2 after the last look-up: 16 blocks at a time.
-  const int nmine = max(0, (v1 - v0 - warp + kWarps - 1) / kWarps);
+  const int nmine = ok ? max(0, (v1 - v0 - warp + kWarps - 1) / kWarps) : 0;
   const int32_t* table = p.table + b * p.table_stride;
-  uint64_t at = 0;    // V rows of those 16 tokens, 0 where there is no page
-  int at_off = 0;     // their offset in the page
+  PageAt at{-1, 0};
   uint32_t seen = 0;  // two bits per stage: which halves of the block have a page
-  const int dp = FULL ? CH : cv.dp;
-  constexpr int PPR = S::kRow / 16;   // pieces of a V row
-  constexpr int RPI = 32 / PPR;       // rows that the warp copies per instruction
-  const int vrow = lane / PPR, vcol = lane % PPR;
-  const bool vok = FULL || vcol * 16 < dp;
-  const int vsrc = vrow * dp + vcol * 16;
-  // The half's other pieces: 16 sign rows, two pieces of mu, one of exponents, at a distance of
-  // xsrc + offset * xmul from its V rows.
-  const int xsrc = lane < 16 ? cv.off_bits() + lane * 16 : (lane < 18 ? cv.off_mu() + (lane - 16) * 16 : cv.off_exp());
-  const int xsize = lane < 16 ? 16 : (lane < 18 ? 2 : 1);
-  const int xmul = xsize - dp;
-  const uint32_t xdst = lane < 16 ? lane * 16 : (lane < 18 ? S::xMu + (lane - 16) * 16 : S::xExp);
-  auto issue = [&](int n, int st) {
-    if (n < nmine) {
-      if ((n & 15) == 0) {
-        at = 0;
-        const int m = n + (lane >> 1);
-        if (m < nmine) {
-          const PageAt pg = page_at(p, table, w.kv, w.block_at(v0 + warp + m * kWarps) * kBlk + (lane & 1) * kPageUnit);
-          at_off = pg.off;
-          if (pg.page >= 0) at = reinterpret_cast<uint64_t>(cv.block(pg.page, head)) + pg.off * dp;
-        }
-      }
-      const uint32_t dst = vring + st * S::kV, extra = xring + st * S::kX + xdst;
-      uint32_t ok2 = 0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint64_t rows = __shfl_sync(0xffffffffu, at, 2 * (n & 15) + h);
-        const int off = __shfl_sync(0xffffffffu, at_off, 2 * (n & 15) + h);
-        const uint32_t to = dst + kPageUnit * h * S::kRow;
-        if (rows != 0) {
-          ok2 |= 1u << h;
-          const uint8_t* src = reinterpret_cast<const uint8_t*>(rows);
-          if (vok) {
-#pragma unroll
-            for (int i = 0; i < kPageUnit / RPI; ++i)
-              cp_async16(to + S::piece(i * RPI + vrow, vcol), src + vsrc + i * RPI * dp);
-          }
-          if (lane < 19) cp_async16(extra + kPageUnit * h * xsize, src + xsrc + off * xmul);
-        } else {
-          // No page: the rows are not seen, and their weights of 0 need finite scales.
-          if (lane < 19) sts128(extra + kPageUnit * h * xsize, 0u, 0u, 0u, 0u);
-        }
-      }
-      seen = (seen & ~(3u << (2 * st))) | (ok2 << (2 * st));
+  // Copies of a block: lane 4 h + k brings, of its half h, the V rows (k = 0), the sign rows, mu or
+  // the exponents, which lie at off + offset * size in the page's block.
+  const int half = (lane >> 2) & 1, kind = lane & 3;
+  const int xoff = kind == 1 ? cv.off_bits() : (kind == 2 ? cv.off_mu() : cv.off_exp());
+  const int xsize = kind == 1 ? 16 : (kind == 2 ? 2 : 1);
+  const int xdst = (kind == 1 ? 0 : (kind == 2 ? S::xMu : S::xExp)) + kPageUnit * half * xsize;
+  auto issue = [&](int n, int to) {  // block n of the warp into stage `to`
+    if (n >= nmine) return;
+    if ((n & 15) == 0) {
+      at.page = -1;
+      const int m = n + (lane >> 1);
+      if (m < nmine) at = page_at(p, table, w.kv, w.block_at(v0 + warp + m * kWarps) * kBlk + (lane & 1) * kPageUnit);
     }
-    cp_async_commit();
+    const int page = __shfl_sync(0xffffffffu, at.page, 2 * (n & 15) + half);
+    const int off = __shfl_sync(0xffffffffu, at.off, 2 * (n & 15) + half);
+    // Bit 4 h of the vote: the half h has a page.
+    const uint32_t vote = __ballot_sync(0xffffffffu, page >= 0);
+    const uint32_t have = (vote & 1u) | ((vote >> 3) & 2u);
+    const uint32_t bar = smem_u32(&s_full[warp][to]), extra = xring + to * S::kX + xdst;
+    if (lane == 0) mbar_arrive_expect_tx(&s_full[warp][to], ((have & 1u) + (have >> 1)) * S::kHalf);
+    __syncwarp();
+    if (lane < 8) {
+      if (page < 0) {
+        // No page: the rows are not seen, but what their scores are made of stays finite.
+        if (kind > 0)
+          for (int i = 0; i < xsize; ++i) sts128(extra + 16 * i, 0u, 0u, 0u, 0u);
+      } else if (kind == 0) {
+        tma_load_3d(vring + to * S::kV + kPageUnit * half * S::kRow, &v_map, bar, 0, off, page * cv.heads + head);
+      } else {
+        bulk_load(extra, cv.block(page, head) + xoff + off * xsize, kPageUnit * xsize, bar);
+      }
+    }
+    seen = (seen & ~(3u << (2 * to))) | (have << (2 * to));
   };
 #pragma unroll
-  for (int n = 0; n < kStages - 1; ++n) issue(n, n);
+  for (int n = 0; n < kStages; ++n) issue(n, st + n >= kStages ? st + n - kStages : st + n);
 
   // Sign bits and scale of the rows, while the first blocks are on their way.
   for (int r = warp; r < R; r += kWarps) {
@@ -268,185 +300,190 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 3) paged_decode_kernel
   }
   __syncthreads();
 
-  // Q as the A operand: this thread's bytes meet word t of the keys; byte i of step s is channel
-  // 32 t + 8 i + s, and holds +-2^(6 - s) (s = 7: +-1, its bit is moved down by one).
-  uint32_t qa[NR][8];
-  float cq[NR], qsum[NR];
-  int last[NR], wlo[NR];  // the row sees keys j <= last with j >= wlo or j < sinks
+  // Q as the B operand, row g: this thread's bytes meet word t of the keys; byte i of step s is
+  // channel 32 t + 8 i + s, and holds +-2^(6 - s) (s = 7: +-1, its bit is moved down by one).
+  uint32_t qb[NR][8];
+  // Of the rows 2 t and 2 t + 1, which this thread's scores belong to:
+  float2 cq[NR], back[NR];
+  int last[NR][2], wlo[NR][2];  // the row sees keys j <= last with j >= wlo or j < sinks
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
-    const int r = 8 * n + g;
-    const uint32_t word = s_bits[r][t];
+    const uint32_t word = s_bits[8 * n + g][t];
     const int nc = cv.d - 32 * t;  // channels of this word
     const uint32_t live = nc >= 32 ? 0xffffffffu : (nc <= 0 ? 0u : (1u << nc) - 1u);
 #pragma unroll
-    for (int st = 0; st < 8; ++st) {
+    for (int s = 0; s < 8; ++s) {
       // Bytes mag, or 256 - mag where the bit is set; 0 where there is no channel.
-      const uint32_t mag = 1u << (st == 7 ? 0 : 6 - st);
-      qa[n][st] = (0x01010101u * mag + ((word >> st) & 0x01010101u) * (256u - 2u * mag)) &
-                  (((live >> st) & 0x01010101u) * 255u);
+      const uint32_t mag = 1u << (s == 7 ? 0 : 6 - s);
+      qb[n][s] = (0x01010101u * mag + ((word >> s) & 0x01010101u) * (256u - 2u * mag)) &
+                 (((live >> s) & 0x01010101u) * 255u);
     }
-    const int neg = __popc(s_bits[r][0]) + __popc(s_bits[r][1]) + __popc(s_bits[r][2]) + __popc(s_bits[r][3]);
-    qsum[n] = static_cast<float>(cv.d - 2 * neg);
-    cq[n] = p.scale_log2 * s_mu[r];
-    const int pos = w.pos0() + (w.r0 + r) / p.group;
-    last[n] = r < w.rows ? (p.causal ? min(pos, w.kv - 1) : w.kv - 1) : -1;
-    wlo[n] = p.causal && p.window > 0 ? pos - p.window + 1 : 0;
+    float c2[2], b2[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 8 * n + 2 * t + i;
+      const int neg = __popc(s_bits[r][0]) + __popc(s_bits[r][1]) + __popc(s_bits[r][2]) + __popc(s_bits[r][3]);
+      b2[i] = static_cast<float>(cv.d - 2 * neg) + kMagic / 32.0f;
+      c2[i] = p.scale_log2 * s_mu[r];
+      const int pos = w.pos0() + (w.r0 + r) / p.group;
+      last[n][i] = r < w.rows ? (p.causal ? min(pos, w.kv - 1) : w.kv - 1) : -1;
+      wlo[n][i] = p.causal && p.window > 0 ? pos - p.window + 1 : 0;
+    }
+    cq[n] = make_float2(c2[0], c2[1]);
+    back[n] = make_float2(b2[0], b2[1]);
   }
   // What every row of the tile sees: keys <= all_last from all_lo on.
   const int all_last = p.causal ? min(w.pos0() + w.r0 / p.group, w.kv - 1) : w.kv - 1;
   const int all_lo = p.causal && p.window > 0 ? w.pos0() + (w.r0 + w.rows - 1) / p.group - p.window + 1 : 0;
 
   float acc[NR][MT][4];
-  float M[NR];
-  float2 l[NR];
+  float2 M[NR], l[NR];  // of the rows 2 t and 2 t + 1
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
-    M[n] = -CUDART_INF_F;
+    M[n] = make_float2(-CUDART_INF_F, -CUDART_INF_F);
     l[n] = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][m][i] = 0.0f;
   }
-  // Key of column g of the first of two score products of 16 keys (the second: two further on), such
-  // that a thread's four scores are the keys 4 t .. 4 t + 3.
-  const uint32_t kword = (4 * (g >> 1) + (g & 1)) * 16 + 4 * t;
+  // Keys of this thread's scores: 16 h + key0 + 2 k. (Row g of an 8 x 8 matrix is the key
+  // 4 (g / 2) + g % 2, the second matrix two further on, so that the turned matrices hold the keys
+  // 4 t .. 4 t + 3 as ldmatrix holds V's.)
+  const int key0 = 4 * (g >> 1) + (g & 1);
   // Row of V that this lane gives to ldmatrix: tile 0's piece of key `lane`; tile m's is the same
-  // address with the bits of 16 m flipped (stages start on 128 bytes).
+  // address with the bits of 16 m flipped.
   const uint32_t vbase = vring + S::piece(lane, 0);
   int start[4];  // a register quad of its own for the products' start
 #pragma unroll
   for (int i = 0; i < 4; ++i) asm volatile("mov.u32 %0, %1;" : "=r"(start[i]) : "n"(kMagicBits));
 
-  int st = 0;
-  for (int n = 0; n < nmine; ++n) {
-    cp_async_wait<kStages - 2>();
-    __syncwarp();
-    issue(n + kStages - 1, st == 0 ? kStages - 1 : st - 1);  // into the stage that the last block left
+  for (int n = 0; n < nmine && ok; ++n) {
     const uint32_t stage = st * S::kV, fl = xring + st * S::kX;
     const int j0 = w.block_at(v0 + warp + n * kWarps) * kBlk;
-    const uint32_t ok2 = (seen >> (2 * st)) & 3u;
-    st = st == kStages - 1 ? 0 : st + 1;
+    ok = __all_sync(0xffffffffu, wait_stage(&s_full[warp][st], (phase >> st) & 1u));
+    if (!ok) break;
+    phase ^= 1u << st;
+    const uint32_t have = (seen >> (2 * st)) & 3u;
     uint32_t word[2][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) word[h][k] = lds32(fl + kword + (16 * h + 2 * k) * 16);
+      for (int k = 0; k < 2; ++k) word[h][k] = lds32(fl + (16 * h + key0 + 2 * k) * 16 + 4 * t);
     {
       const int e = static_cast<int8_t>(lds16(fl + S::xExp + (lane & ~1)) >> (8 * (lane & 1)));
       const int ec = min(max(e, kMinExp), kMaxExp);
-      const float mu = __uint_as_float(lds16(fl + S::xMu + 2 * lane) << 16);
+      const uint32_t mu = lds16(fl + S::xMu + 2 * lane) << 16;
       __syncwarp();
-      sts_f32(fl + 4 * lane, mu);
-      sts_f32(fl + 4 * (kBlk + lane), static_cast<float>(ec));
-      sts_f32(fl + 4 * (2 * kBlk + lane), __uint_as_float(static_cast<uint32_t>(127 - ec) << 23));
+      sts128(fl + 16 * lane, mu, __float_as_uint(static_cast<float>(ec)), static_cast<uint32_t>(127 - ec) << 23, 0u);
     }
-    // 64 sum q k of 16 keys each (h), keys 4 t .. 4 t + 3 of them in the order 0, 1 | 2, 3.
-    int x[2][2][4];
+    // 64 sum q k of 16 keys each (h) and 8 rows.
+    int x[NR][2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const uint32_t a0 = word[h][0] & (0x01010101u << (2 * s)), a1 = word[h][1] & (0x01010101u << (2 * s));
+        const uint32_t a2 = s == 3 ? (word[h][0] >> 1) & 0x40404040u : word[h][0] & (0x02020202u << (2 * s));
+        const uint32_t a3 = s == 3 ? (word[h][1] >> 1) & 0x40404040u : word[h][1] & (0x02020202u << (2 * s));
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          if (s == 0)
+            mma_qk_first(x[r][h], start, a0, a1, a2, a3, qb[r][0], qb[r][1]);
+          else
+            mma_qk(x[r][h], a0, a1, a2, a3, qb[r][2 * s], qb[r][2 * s + 1]);
+        }
+      }
+    __syncwarp();
+    // Scores + e of the key 16 h + key0 + 2 k and the rows 2 t and 2 t + 1.
+    float2 sc[NR][2][2];
+    float down[2][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        mma_i8_first(x[h][k], start, qa[0][0], NR == 2 ? qa[NR - 1][0] : 0u, qa[0][1], NR == 2 ? qa[NR - 1][1] : 0u,
-                     word[h][k] & 0x01010101u, word[h][k] & 0x02020202u);
+        const float4 f = lds_f4(fl + (16 * h + key0 + 2 * k) * 16);
+        down[h][k] = f.z;
 #pragma unroll
-        for (int s = 1; s < 4; ++s)
-          mma_i8(x[h][k], qa[0][2 * s], NR == 2 ? qa[NR - 1][2 * s] : 0u, qa[0][2 * s + 1],
-                 NR == 2 ? qa[NR - 1][2 * s + 1] : 0u, word[h][k] & (0x01010101u << (2 * s)),
-                 s == 3 ? (word[h][k] >> 1) & 0x40404040u : word[h][k] & (0x02020202u << (2 * s)));
-      }
-    __syncwarp();
-    // Scores + e: sc[r][h][k] holds the keys 16 h + 4 t + 2 k and the next.
-    float2 sc[NR][2][2], down[2][2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 mu = lds_f4(fl + 64 * h + 16 * t), e = lds_f4(fl + 4 * kBlk + 64 * h + 16 * t),
-                   dn = lds_f4(fl + 8 * kBlk + 64 * h + 16 * t);
-      const float2 mu2[2] = {make_float2(mu.x, mu.y), make_float2(mu.z, mu.w)};
-      const float2 e2[2] = {make_float2(e.x, e.y), make_float2(e.z, e.w)};
-      down[h][0] = make_float2(dn.x, dn.y);
-      down[h][1] = make_float2(dn.z, dn.w);
-#pragma unroll
-      for (int r = 0; r < NR; ++r)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int r = 0; r < NR; ++r) {
           // x = sum q - 2 sum q k: exact, the constant of the accumulator's start taken off with it.
-          const float back = qsum[r] + kMagic / 32.0f;
-          const float2 y = __ffma2_rn(make_float2(__int_as_float(x[h][k][2 * r]), __int_as_float(x[h][k][2 * r + 1])),
-                                      make_float2(-0.03125f, -0.03125f), make_float2(back, back));
-          sc[r][h][k] = __ffma2_rn(__fmul2_rn(y, mu2[k]), make_float2(cq[r], cq[r]), e2[k]);
+          float2 y = __ffma2_rn(make_float2(__int_as_float(x[r][h][2 * k]), __int_as_float(x[r][h][2 * k + 1])),
+                                make_float2(-0.03125f, -0.03125f), back[r]);
+          y = __fmul2_rn(y, cq[r]);
+          sc[r][h][k] = make_float2(__fmaf_rn(y.x, f.x, f.y), __fmaf_rn(y.y, f.x, f.y));
         }
-    }
-    if (!(ok2 == 3u && j0 + kBlk - 1 <= all_last && j0 >= all_lo)) {
+      }
+    if (!(have == 3u && j0 + kBlk - 1 <= all_last && j0 >= all_lo)) {
 #pragma unroll
       for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int j = j0 + 16 * h + 4 * t + k;
-            const bool see = ((ok2 >> h) & 1u) && j <= last[r] && (j >= wlo[r] || j < p.sinks);
-            float& v = (k & 1) ? sc[r][h][k >> 1].y : sc[r][h][k >> 1].x;
-            if (!see) v = -CUDART_INF_F;
+          for (int k = 0; k < 2; ++k) {
+            const int j = j0 + 16 * h + key0 + 2 * k;
+            const bool in = (have >> h) & 1u, sink = j < p.sinks;
+            if (!(in && j <= last[r][0] && (j >= wlo[r][0] || sink))) sc[r][h][k].x = -CUDART_INF_F;
+            if (!(in && j <= last[r][1] && (j >= wlo[r][1] || sink))) sc[r][h][k].y = -CUDART_INF_F;
           }
     }
-    uint32_t bw[NR][2][2];  // weights: high and low bytes of the keys 16 h + 4 t .. + 3
+    uint32_t bw[NR][2][2];  // weights of row g: high and low bytes of the keys 16 h + 4 t .. + 3
     float2 f2[NR];          // what they count, for the rows 2 t and 2 t + 1
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      float mx = fmaxf(fmaxf(fmaxf(sc[r][0][0].x, sc[r][0][0].y), fmaxf(sc[r][0][1].x, sc[r][0][1].y)),
-                       fmaxf(fmaxf(sc[r][1][0].x, sc[r][1][0].y), fmaxf(sc[r][1][1].x, sc[r][1][1].y)));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      if (__any_sync(0xffffffffu, mx > M[r] + kSlack)) {
-        const float to = mx > M[r] + kSlack ? mx : M[r];
-        const float f = M[r] == -CUDART_INF_F ? 0.0f : ex2(M[r] - to);
+      float2 mx = make_float2(fmaxf(fmaxf(sc[r][0][0].x, sc[r][0][1].x), fmaxf(sc[r][1][0].x, sc[r][1][1].x)),
+                              fmaxf(fmaxf(sc[r][0][0].y, sc[r][0][1].y), fmaxf(sc[r][1][0].y, sc[r][1][1].y)));
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, o));
+        mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, o));
+      }
+      if (__any_sync(0xffffffffu, mx.x > M[r].x + kSlack || mx.y > M[r].y + kSlack)) {
+        const float2 to = make_float2(mx.x > M[r].x + kSlack ? mx.x : M[r].x, mx.y > M[r].y + kSlack ? mx.y : M[r].y);
+        const float2 f = make_float2(M[r].x == -CUDART_INF_F ? 0.0f : ex2(M[r].x - to.x),
+                                     M[r].y == -CUDART_INF_F ? 0.0f : ex2(M[r].y - to.y));
         M[r] = to;
-        l[r].x *= f;
-        l[r].y *= f;
-        const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+        l[r] = __fmul2_rn(l[r], f);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          acc[r][m][0] *= f0;
-          acc[r][m][1] *= f1;
-          acc[r][m][2] *= f0;
-          acc[r][m][3] *= f1;
+          acc[r][m][0] *= f.x;
+          acc[r][m][1] *= f.y;
+          acc[r][m][2] *= f.x;
+          acc[r][m][3] *= f.y;
         }
       }
-      const bool none = mx == -CUDART_INF_F;  // the row sees nothing of the block
-      const float ref = none ? 0.0f : -mx, f = none ? 0.0f : ex2(mx - M[r]);
+      // A row that sees nothing of the block has weights 0 (2^-inf) and counts for nothing.
+      const float2 ref = make_float2(mx.x == -CUDART_INF_F ? 0.0f : -mx.x, mx.y == -CUDART_INF_F ? 0.0f : -mx.y);
+      const float2 f = make_float2(mx.x == -CUDART_INF_F ? 0.0f : ex2(mx.x - M[r].x),
+                                   mx.y == -CUDART_INF_F ? 0.0f : ex2(mx.y - M[r].y));
       float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t w16[4];
+        uint32_t w16[2];  // 16-bit weights of the keys 16 h + 4 t + 2 k and the next, of row g
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float2 y = __fadd2_rn(sc[r][h][k], make_float2(ref, ref));
+          const float2 y = __fadd2_rn(sc[r][h][k], ref);
           const float2 e = make_float2(ex2(y.x), ex2(y.y));
-          sum = __ffma2_rn(e, down[h][k], sum);
+          sum.x = __fmaf_rn(e.x, down[h][k], sum.x);
+          sum.y = __fmaf_rn(e.y, down[h][k], sum.y);
           const float2 z = __ffma2_rn(e, make_float2(kUnit, kUnit), make_float2(kMagic, kMagic));
-          w16[2 * k] = __float_as_uint(z.x);
-          w16[2 * k + 1] = __float_as_uint(z.y);
+          w16[k] = turn8(__byte_perm(__float_as_uint(z.x), __float_as_uint(z.y), 0x5410));
         }
-        const uint32_t u = __byte_perm(w16[0], w16[1], 0x5140), v = __byte_perm(w16[2], w16[3], 0x5140);
-        bw[r][1][h] = __byte_perm(u, v, 0x5410);
-        bw[r][0][h] = __byte_perm(u, v, 0x7632);
+        bw[r][0][h] = __byte_perm(w16[0], w16[1], 0x7531);
+        bw[r][1][h] = __byte_perm(w16[0], w16[1], 0x6420);
       }
-      l[r] = __ffma2_rn(sum, make_float2(f, f), l[r]);
-      const float fu = f * (1.0f / kUnit);
-      f2[r] = make_float2(__shfl_sync(0xffffffffu, fu, 8 * t), __shfl_sync(0xffffffffu, fu, 8 * t + 4));
+      l[r] = __ffma2_rn(sum, f, l[r]);
+      f2[r] = __fmul2_rn(f, make_float2(1.0f / kUnit, 1.0f / kUnit));
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      if (FULL || 16 * m < cv.dp) {
+      if (16 * m < dp) {
         uint32_t a[4];  // channels g and g + 8 of the tile: keys 4 t .. + 3 of the block's halves
         ldmatrix_t8((vbase + stage) ^ (m * 16), a);
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           int hi[4], lo[4];
-          mma_i8_first(hi, start, a[0], a[1], a[2], a[3], bw[r][0][0], bw[r][0][1]);
-          mma_i8_first(lo, start, a[0], a[1], a[2], a[3], bw[r][1][0], bw[r][1][1]);
+          mma_pv(hi, start, a[0], a[1], a[2], a[3], bw[r][0][0], bw[r][0][1]);
+          mma_pv(lo, start, a[0], a[1], a[2], a[3], bw[r][1][0], bw[r][1][1]);
 #pragma unroll
           for (int i = 0; i < 4; i += 2) {
             float2 o = make_float2(acc[r][m][i], acc[r][m][i + 1]);
@@ -458,9 +495,15 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 3) paged_decode_kernel
         }
       }
     }
+    // The stage's next block: what this warp wrote there comes before what the copies write.
+    fence_proxy_async_smem();
     __syncwarp();
+    issue(n + kStages, st);
+    st = st == kStages - 1 ? 0 : st + 1;
   }
-  cp_async_wait<0>();
+  // After a timeout: the copies still on their way get one more limited wait.
+  if (!ok)
+    for (int n = 0; n < min(nmine, kStages); ++n) wait_stage(&s_full[warp][n], (phase >> n) & 1u);
   __syncthreads();
 
   // Join the warps: each leaves its (M, l) and its sums in shared memory. A thread holds, for the
@@ -468,10 +511,16 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 3) paged_decode_kernel
   float* s_o = reinterpret_cast<float*>(smem);  // [kWarps][R][CH]
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
-    float sum = l[n].x + l[n].y;
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    if (t == 0) s_ml[warp][8 * n + g] = make_float2(M[n], sum);
+    float2 sum = l[n];
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      sum.x += __shfl_xor_sync(0xffffffffu, sum.x, o);
+      sum.y += __shfl_xor_sync(0xffffffffu, sum.y, o);
+    }
+    if (g == 0) {
+      s_ml[warp][8 * n + 2 * t] = make_float2(M[n].x, sum.x);
+      s_ml[warp][8 * n + 2 * t + 1] = make_float2(M[n].y, sum.y);
+    }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -507,7 +556,9 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 3) paged_decode_kernel
         p.lse[row] = lr > 0.0f ? (Mr + log2f(lr)) * CUDART_LN2_F : -CUDART_INF_F;
     }
   }
-  __syncthreads();  // before the next (tile, head) uses the shared memory
+  // Before the next (tile, head) uses the shared memory, by copies too.
+  fence_proxy_async_smem();
+  __syncthreads();
   }
 }
 
@@ -613,15 +664,30 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(PagedAttnParams p,
   if (c == 0 && p.lse != nullptr) p.lse[row] = lt > 0.0f ? (M + log2f(lt)) * CUDART_LN2_F : -CUDART_INF_F;
 }
 
-template <int CPG, int NR, bool FULL>
-cudaError_t launch_decode_full(const PagedAttnParams& p, int dt, cudaStream_t s) {
-  constexpr int ring = kWarps * Ring<CPG>::kBytes, out = kWarps * 8 * NR * CPG * 8 * 4;
-  constexpr int smem = ring > out ? ring : out;
-  auto kernel = paged_decode_kernel<CPG, NR, FULL>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <int CPG, int NR>
+cudaError_t launch_decode(const PagedAttnParams& p, int dt, cudaStream_t s) {
+  static_assert(kWarps * 8 * NR * CPG * 8 * 4 <= kWarps * Ring<CPG>::kBytes, "the warps' sums replace their rings");
+  constexpr int smem = Ring<CPG>::total(8 * NR);
+  cudaError_t e = allow_smem<paged_decode_kernel<CPG, NR>>(smem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = static_cast<int64_t>(p.B) * p.row_tiles * p.cache.heads;
-  kernel<<<static_cast<unsigned>(p.ctas > 0 ? p.ctas : tiles), kThreads, smem, s>>>(p, dt == BA_F16 ? 1 : 0);
+  // The V rows of all blocks, as (byte, token, block); a copy brings 16 rows, padded to CPG * 8 bytes.
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return cudaErrorNotSupported;
+  const CacheView& cv = p.cache;
+  CUtensorMap map{};
+  if (cv.num_pages > 0) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cv.dp), static_cast<cuuint64_t>(cv.page_size),
+                                static_cast<cuuint64_t>(cv.num_pages) * cv.heads};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cv.dp), static_cast<cuuint64_t>(cv.block_bytes)};
+    const cuuint32_t box[3] = {CPG * 8, kPageUnit, 1}, step[3] = {1, 1, 1};
+    if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, cv.data, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CPG == 16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  const int64_t tiles = static_cast<int64_t>(p.B) * p.row_tiles * cv.heads;
+  paged_decode_kernel<CPG, NR><<<static_cast<unsigned>(p.ctas > 0 ? p.ctas : tiles), kThreads, smem, s>>>(
+      p, dt == BA_F16 ? 1 : 0, map);
   if ((e = cudaGetLastError()) != cudaSuccess || p.ctas == 0) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.ctas * p.row_tile));
@@ -633,12 +699,6 @@ cudaError_t launch_decode_full(const PagedAttnParams& p, int dt, cudaStream_t s)
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, line_join_kernel, p, kBlk);
-}
-
-template <int CPG, int NR>
-cudaError_t launch_decode(const PagedAttnParams& p, int dt, cudaStream_t s) {
-  return p.cache.dp == CPG * 8 ? launch_decode_full<CPG, NR, true>(p, dt, s)
-                               : launch_decode_full<CPG, NR, false>(p, dt, s);
 }
 
 }  // namespace
@@ -671,6 +731,10 @@ int paged_decode_ctas(const PagedAttnParams& p, int sms) {
   if (blocks <= 2 * kWarps) return 0;
   // As many CTAs as fit at once (by registers), each with one block per warp at least.
   return static_cast<int>(std::min<int64_t>(sms * (p.row_tile == 8 ? 4 : 3), ceil_div((blocks + kCost) * tiles, kWarps)));
+}
+
+cudaError_t read_and_clear_decode_status(int* value, cudaStream_t s) {
+  return read_and_clear_status(g_decode_status, value, s);
 }
 
 }  // namespace binattn

@@ -46,11 +46,11 @@
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
-#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
 #include "tc_ptx.cuh"
+#include "tensormap.h"
 
 namespace binattn {
 
@@ -1227,23 +1227,6 @@ __global__ void __launch_bounds__(Cfg<DP, BK>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  });
-  return fn;
 }
 
 constexpr int kMaxSmem = 227 * 1024;  // per CTA

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace binattn {
@@ -87,8 +89,32 @@ cudaError_t launch_attn_tc(const AttnParams& p, cudaStream_t s);
 // BA_OK, or BA_ERR_CUDA with e kept for ba_last_cuda_error() on this thread.
 ba_status report_cuda(cudaError_t e);
 
-// Device status word of the kernels with bounded waits.
+// Device status words of the kernels with bounded waits.
 cudaError_t read_and_clear_device_status(int* value, cudaStream_t s);
-cudaError_t read_and_clear_paged_status(int* value, cudaStream_t s);
+cudaError_t read_and_clear_chunk_status(int* value, cudaStream_t s);
+cudaError_t read_and_clear_decode_status(int* value, cudaStream_t s);
+
+// Allows a kernel its dynamic shared memory, once per device.
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (e != cudaSuccess || (done.load() & bit) != 0) return e;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit);
+  return e;
+}
+
+template <typename Symbol>
+cudaError_t read_and_clear_status(Symbol& symbol, int* value, cudaStream_t s) {
+  cudaError_t e = cudaMemcpyFromSymbolAsync(value, symbol, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  if (e != cudaSuccess) return e;
+  if ((e = cudaStreamSynchronize(s)) != cudaSuccess) return e;
+  const int zero = 0;
+  if ((e = cudaMemcpyToSymbolAsync(symbol, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s)) != cudaSuccess) return e;
+  return cudaStreamSynchronize(s);
+}
 
 }  // namespace binattn

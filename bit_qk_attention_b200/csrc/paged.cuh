@@ -133,9 +133,11 @@ struct Stretch {
 };
 
 template <int THREADS>
-__device__ __forceinline__ Stretch find_stretch(const PagedAttnParams& p, int bk, int cost, int min_units) {
-  __shared__ int64_t s_warp[THREADS / 32], s_base;
-  __shared__ int s_entry;
+__device__ __forceinline__ Stretch find_stretch(const PagedAttnParams& p, int bk, int cost, int min_units,
+                                                int64_t* scratch) {  // shared memory: THREADS / 32 + 2
+  int64_t* s_warp = scratch;
+  int64_t& s_base = scratch[THREADS / 32];
+  int64_t& s_entry = scratch[THREADS / 32 + 1];
   const int heads = p.cache.heads, n = p.B * p.row_tiles, each = (n + THREADS - 1) / THREADS;
   const int i0 = min(n, static_cast<int>(threadIdx.x) * each), i1 = min(n, i0 + each);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -172,7 +174,7 @@ __device__ __forceinline__ Stretch find_stretch(const PagedAttnParams& p, int bk
     s_base = base;
   }
   __syncthreads();
-  st.entry = s_entry;
+  st.entry = static_cast<int>(s_entry);
   st.base = s_base;
   return st;
 }
