@@ -111,7 +111,7 @@ ba_status plan(const ba_kv_cache* cache, const ba_paged_seqs* s, PagedAttnParams
       *ws = align_up(n * p->cache.dp * 4) + align_up(n * 8);
     }
   } else {
-    p->ctas = paged_decode_ctas(*p, sm_count());
+    paged_decode_plan(p, sm_count());
     if (p->ctas > 0) *ws = line_workspace(*p, nullptr);
   }
   return BA_OK;

@@ -50,6 +50,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kBlk = 32;       // keys per stage of a warp
 constexpr int kStages = 3;
 constexpr int kCost = 12;       // blocks that a CTA could do while it starts and ends a (tile, head)
+constexpr int kShort = 4;       // blocks of a warp that the joining launch costs
 constexpr float kSlack = 40.0f;  // log2 by which a block's maximum may pass the reference
 constexpr float kUnit = 65280.0f;  // weight 1 in fixed point: 255 * 256
 constexpr int kMagicBits = 0x4B400000;  // 1.5 * 2^23
@@ -151,6 +152,18 @@ __device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity) {
   return true;
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// A float at the shared-memory address `a` of the cluster's CTA `rank`.
+__device__ __forceinline__ float lds_cluster(uint32_t a, int rank) {
+  uint32_t at;
+  float x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+  return x;
+}
+
 // One row of q by a warp: sign words and sum of |x|.
 template <typename T>
 __device__ __forceinline__ void scan_row(const T* src, int d, int lane, uint32_t (&word)[4], float& sum) {
@@ -202,14 +215,17 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 3)
       return;
     }
   } else {
-    line.entry = blockIdx.x / cv.heads;
+    line.entry = blockIdx.x / p.cluster / cv.heads;
   }
+
+  // One (tile, head) per cluster: its CTAs take equal parts and join them through their shared memory.
+  const int rank = p.ctas > 0 ? 0 : blockIdx.x % p.cluster;
 
   for (bool more = true; more;) {
   // The next (tile, head) of the CTA: its blocks v0 .. v1 - 1 of all.
   const RowTile w = entry_tile(p, line.entry, kBlk);
   const int b = line.entry / p.row_tiles;
-  int head = blockIdx.x % cv.heads, v0 = 0, v1 = w.nblk, slot = -1;  // slot -1: nothing is cut
+  int head = blockIdx.x / p.cluster % cv.heads, v0 = 0, v1 = w.nblk, slot = -1;  // slot -1: nothing is cut
   if (p.ctas > 0) {
     const int units = units_of(w, kCost);
     if (units == 0) {  // a tile without rows
@@ -238,6 +254,8 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 3)
   } else {
     more = false;
     if (w.rows <= 0) return;
+    v0 = static_cast<int>(static_cast<int64_t>(w.nblk) * rank / p.cluster);
+    v1 = static_cast<int>(static_cast<int64_t>(w.nblk) * (rank + 1) / p.cluster);
   }
 
   // The warp's blocks are v0 + warp, v0 + warp + kWarps, ... Lane l keeps the page and the offset
@@ -509,6 +527,9 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 3)
   // Join the warps: each leaves its (M, l) and its sums in shared memory. A thread holds, for the
   // rows 8 n + 2 t and 8 n + 2 t + 1, the channels 16 m + g and 16 m + g + 8.
   float* s_o = reinterpret_cast<float*>(smem);  // [kWarps][R][CH]
+  float* s_sum = s_o + kWarps * R * CH;         // [R][CH], and (M, l) of the rows: what a cluster joins
+  float2* s_fin = reinterpret_cast<float2*>(s_sum + R * CH);
+  const bool clustered = p.ctas == 0 && p.cluster > 1;
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
     float2 sum = l[n];
@@ -546,15 +567,47 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 3)
       for (int k = 0; k < kWarps; ++k) x += f[k] * s_o[(k * R + r) * CH + c];
       if (slot >= 0)
         p.part_o[part * dp + c] = x;
+      else if (clustered)
+        s_sum[r * CH + c] = x;
       else if (c < cv.d)
         store_out(p.o, row * cv.d + c, x * inv, p.o_dt);
     }
     if (lane == 0) {
       if (slot >= 0)
         p.part_ml[part] = make_float2(Mr, lr);
+      else if (clustered)
+        s_fin[r] = make_float2(Mr, lr);
       else if (p.lse != nullptr)
         p.lse[row] = lr > 0.0f ? (Mr + log2f(lr)) * CUDART_LN2_F : -CUDART_INF_F;
     }
+  }
+  if (clustered) {
+    // Rows of the tile by turns: each CTA joins all parts of its rows.
+    cluster_arrive();
+    cluster_wait();
+    for (int r = rank + p.cluster * warp; r < w.rows; r += p.cluster * kWarps) {
+      float Mr = -CUDART_INF_F, lr = 0.0f, x[CH / 32];
+#pragma unroll
+      for (int i = 0; i < CH / 32; ++i) x[i] = 0.0f;
+      for (int k = 0; k < p.cluster; ++k) Mr = fmaxf(Mr, lds_cluster(smem_u32(&s_fin[r]), k));
+      for (int k = 0; k < p.cluster; ++k) {
+        const float Mk = lds_cluster(smem_u32(&s_fin[r]), k);
+        const float f = Mk == -CUDART_INF_F ? 0.0f : ex2(Mk - Mr);
+        lr = __fmaf_rn(f, lds_cluster(smem_u32(&s_fin[r]) + 4, k), lr);
+#pragma unroll
+        for (int i = 0; i < CH / 32; ++i)
+          x[i] = __fmaf_rn(f, lds_cluster(smem_u32(&s_sum[r * CH + 32 * i + lane]), k), x[i]);
+      }
+      const int64_t row = (w.t0 + (w.r0 + r) / p.group) * p.heads + head * p.group + (w.r0 + r) % p.group;
+      const float inv = lr > 0.0f ? 1.0f / lr : 0.0f;
+#pragma unroll
+      for (int i = 0; i < CH / 32; ++i)
+        if (32 * i + lane < cv.d) store_out(p.o, row * cv.d + 32 * i + lane, x[i] * inv, p.o_dt);
+      if (lane == 0 && p.lse != nullptr) p.lse[row] = lr > 0.0f ? (Mr + log2f(lr)) * CUDART_LN2_F : -CUDART_INF_F;
+    }
+    // No CTA leaves while another reads its shared memory.
+    cluster_arrive();
+    cluster_wait();
   }
   // Before the next (tile, head) uses the shared memory, by copies too.
   fence_proxy_async_smem();
@@ -666,7 +719,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(PagedAttnParams p,
 
 template <int CPG, int NR>
 cudaError_t launch_decode(const PagedAttnParams& p, int dt, cudaStream_t s) {
-  static_assert(kWarps * 8 * NR * CPG * 8 * 4 <= kWarps * Ring<CPG>::kBytes, "the warps' sums replace their rings");
+  static_assert((kWarps + 1) * 8 * NR * CPG * 8 * 4 + 8 * NR * 8 <= kWarps * Ring<CPG>::kBytes, "the warps' sums replace their rings");
   constexpr int smem = Ring<CPG>::total(8 * NR);
   cudaError_t e = allow_smem<paged_decode_kernel<CPG, NR>>(smem);
   if (e != cudaSuccess) return e;
@@ -686,17 +739,25 @@ cudaError_t launch_decode(const PagedAttnParams& p, int dt, cudaStream_t s) {
       return cudaErrorInvalidValue;
   }
   const int64_t tiles = static_cast<int64_t>(p.B) * p.row_tiles * cv.heads;
-  paged_decode_kernel<CPG, NR><<<static_cast<unsigned>(p.ctas > 0 ? p.ctas : tiles), kThreads, smem, s>>>(
-      p, dt == BA_F16 ? 1 : 0, map);
-  if ((e = cudaGetLastError()) != cudaSuccess || p.ctas == 0) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.ctas * p.row_tile));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
   cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(static_cast<unsigned>(p.ctas > 0 ? p.ctas : tiles * p.cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  if (p.ctas == 0 && p.cluster > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.numAttrs = 1;
+  }
+  e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<CPG, NR>, p, dt == BA_F16 ? 1 : 0, map);
+  if (e != cudaSuccess || p.ctas == 0) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.ctas * p.row_tile));
+  cfg.dynamicSmemBytes = 0;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, line_join_kernel, p, kBlk);
 }
@@ -721,16 +782,26 @@ cudaError_t launch_paged_decode(const PagedAttnParams& p, int dt, cudaStream_t s
   return p.row_tile > 8 ? launch_decode<8, 2>(p, dt, s) : launch_decode<8, 1>(p, dt, s);
 }
 
-int paged_decode_ctas(const PagedAttnParams& p, int sms) {
+void paged_decode_plan(PagedAttnParams* p, int sms) {
   // Keys that a tile can see, in blocks.
-  int64_t keys = p.max_kv_len;
-  if (p.causal && p.window > 0)
-    keys = std::min<int64_t>(keys, static_cast<int64_t>(p.window) + p.row_tile + p.sinks + 2 * kBlk);
-  const int64_t blocks = ceil_div(keys, kBlk), tiles = static_cast<int64_t>(p.B) * p.row_tiles * p.cache.heads;
-  // Two blocks per warp or fewer: cutting would cost more (a second launch) than it saves.
-  if (blocks <= 2 * kWarps) return 0;
-  // As many CTAs as fit at once (by registers), each with one block per warp at least.
-  return static_cast<int>(std::min<int64_t>(sms * (p.row_tile == 8 ? 4 : 3), ceil_div((blocks + kCost) * tiles, kWarps)));
+  int64_t keys = p->max_kv_len;
+  if (p->causal && p->window > 0)
+    keys = std::min<int64_t>(keys, static_cast<int64_t>(p->window) + p->row_tile + p->sinks + 2 * kBlk);
+  const int64_t blocks = std::max<int64_t>(1, ceil_div(keys, kBlk));
+  const int64_t tiles = static_cast<int64_t>(p->B) * p->row_tiles * p->cache.heads;
+  const int64_t fit = static_cast<int64_t>(sms) * (p->row_tile == 8 ? 4 : 3);  // CTAs at once, by registers
+  // Short contexts: a cluster of up to eight CTAs per (tile, head), down to a block per warp, joins
+  // its parts itself. Where that leaves a warp more than kShort blocks beyond its share of an even
+  // split over the GPU (or more than kShort of them, when the CTAs do not fit at once and ragged
+  // lengths would leave some SMs waiting), the line of units and its second launch are faster.
+  int cluster = 1;
+  while (cluster < 8 && blocks > cluster * kWarps && tiles * cluster * 2 <= fit) cluster *= 2;
+  const int64_t mine = ceil_div(blocks, cluster * kWarps);
+  const int64_t even = tiles * cluster <= fit ? blocks * tiles / (fit * kWarps) : 0;
+  p->cluster = cluster;
+  p->ctas = 0;
+  if (mine - even > kShort)
+    p->ctas = static_cast<int>(std::min<int64_t>(fit, ceil_div((blocks + kCost) * tiles, kWarps)));
 }
 
 cudaError_t read_and_clear_decode_status(int* value, cudaStream_t s) {

@@ -64,7 +64,8 @@ struct PagedAttnParams {
   int row_tiles;   // tiles of a sequence and KV head (most)
   float* part_o;   // [nsplit][T * heads][dp] unnormalised sums, when nsplit > 1
   float2* part_ml; // [nsplit][T * heads] (maximum in log2, sum)
-  int ctas;          // CTAs that share the line of units; 0: one CTA per (tile, head), nothing is cut
+  int ctas;          // CTAs that share the line of units; 0: a cluster of CTAs per (tile, head)
+  int cluster;       // its size
   JoinNote* notes;   // [ctas]
 };
 
@@ -240,8 +241,8 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 
 cudaError_t launch_paged_decode(const PagedAttnParams& p, int dt, cudaStream_t s);
 cudaError_t launch_paged_chunk(const PagedAttnParams& p, int dt, cudaStream_t s);
-// CTAs that share the work on a device of `sms` SMs (0: one CTA per tile and head).
-int paged_decode_ctas(const PagedAttnParams& p, int sms);
+// Sets p's `ctas` and `cluster` for a device of `sms` SMs.
+void paged_decode_plan(PagedAttnParams* p, int sms);
 int paged_chunk_split_blocks(const PagedAttnParams& p, int sms, int* max_blocks);
 // Second kernel of a split launch: joins the parts of the row tiles (key blocks of bk tokens).
 cudaError_t launch_paged_join(const PagedAttnParams& p, int bk, cudaStream_t s);
