@@ -4,7 +4,7 @@
 // and head, and at HBM's rate a key of 147 bytes leaves an SM some 6.5 cycles. So the work per key
 // is kept small:
 //   * A CTA takes one sequence, one KV head, up to 8 NR rows (new tokens x heads of the group, which
-//     share every key) and a part of the key axis. Each of its warps walks 32-key blocks of its own
+//     share every key) and a part of the key axis. Each of its warps walks 64-key blocks of its own
 //     through a ring of TMA stages (V through a tensor map whose swizzle keeps ldmatrix free of bank
 //     conflicts, the rest as plain bulk copies), with no synchronisation between warps until the end.
 //   * Scores are products of whole numbers on the tensor cores (mma.sync m16n8k32, int8). With K's
@@ -47,10 +47,11 @@ using namespace ptx;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kBlk = 32;       // keys per stage of a warp
-constexpr int kStages = 3;
-constexpr int kCost = 12;       // blocks that a CTA could do while it starts and ends a (tile, head)
-constexpr int kShort = 4;       // blocks of a warp that the joining launch costs
+constexpr int kBlk = 64;       // keys per stage of a warp
+constexpr int kStages = 2;
+constexpr int kQ = kBlk / 16;  // quarters of a block: 16 keys each
+constexpr int kCost = 8;        // blocks that a CTA could do while it starts and ends a (tile, head)
+constexpr int kShort = 3;       // blocks of a warp that the joining launch costs
 constexpr float kSlack = 40.0f;  // log2 by which a block's maximum may pass the reference
 constexpr float kUnit = 65280.0f;  // weight 1 in fixed point: 255 * 256
 constexpr int kMagicBits = 0x4B400000;  // 1.5 * 2^23
@@ -85,14 +86,20 @@ __device__ __forceinline__ void mma_qk(int (&c)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// c = start + A B: A 16 channels x 32 keys of signed codes, B 32 keys x 8 rows of unsigned bytes.
-__device__ __forceinline__ void mma_pv(int (&c)[4], const int (&start)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+// c (+)= A B: A 16 channels x 32 keys of signed codes, B 32 keys x 8 rows of unsigned bytes.
+__device__ __forceinline__ void mma_pv_first(int (&c)[4], const int (&start)[4], const uint32_t (&a)[4], uint32_t b0,
+                                             uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
       : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(start[0]), "r"(start[1]), "r"(start[2]),
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(start[0]), "r"(start[1]), "r"(start[2]),
         "r"(start[3]));
+}
+__device__ __forceinline__ void mma_pv(int (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // Two 16 x 16 matrices of bytes, transposed. Lanes 0-15 and 16-31 give the rows' addresses; the lane
@@ -110,14 +117,14 @@ __device__ __forceinline__ uint32_t turn8(uint32_t x) {
   return y;
 }
 
-// Whole-number results (kMagicBits + n, |n| < 2^22) as floats n.
+// Whole-number results (kMagicBits + n, |n| <= 255 * 128 * 64 < 2^22) as floats n.
 __device__ __forceinline__ float2 whole(int x, int y) {
   return __fadd2_rn(make_float2(__int_as_float(x), __int_as_float(y)), make_float2(-kMagic, -kMagic));
 }
 
 // Shared memory of a warp: V rows of kRow bytes for each stage as the tensor map's swizzle leaves
 // them, then each stage's sign rows, mu and exponents. Once a block's sign rows are read, what its
-// scores need per key as floats (mu, e, 2^-e) takes their place. Four CTAs of four warps just fit an SM.
+// scores need per key as floats (mu, e, 2^-e) takes their place. Three CTAs of four warps just fit an SM.
 template <int CPG>  // eighths of the channels: 16 (rows of 128 bytes) or 8 (rows of 64)
 struct Ring {
   static constexpr int kRow = CPG * 8;
@@ -132,7 +139,7 @@ struct Ring {
   static __host__ __device__ constexpr int offMu(int rows) { return offBits(rows) + rows * 16; }
   static __host__ __device__ constexpr int offScratch(int rows) { return offMu(rows) + rows * 4; }
   static __host__ __device__ constexpr int total(int rows) { return offScratch(rows) + (kWarps + 2) * 8; }
-  static constexpr int kHalf = kPageUnit * (kRow + 16 + 2 + 1);  // bytes that 16 tokens bring
+  static constexpr int kToken = kRow + 16 + 2 + 1;  // bytes that a token brings
   // Byte offset of the 16-byte piece c of key j: the swizzle of 128- or 64-byte rows.
   static __device__ __forceinline__ int piece(int j, int c) {
     return kRow == 128 ? (j * 8 + (c ^ (j & 7))) * 16 : (j * 4 + (c ^ ((j >> 1) & 3))) * 16;
@@ -179,8 +186,8 @@ __device__ __forceinline__ void scan_row(const T* src, int d, int lane, uint32_t
 }
 
 template <int CPG, int NR>
-__global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 3)
-    paged_decode_kernel(PagedAttnParams p, int q_f16, const __grid_constant__ CUtensorMap v_map) {
+__global__ void __launch_bounds__(kThreads, 3)
+    paged_decode_kernel(PagedAttnParams p, int q_f16, int unit, const __grid_constant__ CUtensorMap v_map) {
   using S = Ring<CPG>;
   constexpr int MT = CPG / 2;  // 16-channel tiles
   constexpr int R = 8 * NR;    // rows of a CTA
@@ -258,45 +265,49 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 3)
     v1 = static_cast<int>(static_cast<int64_t>(w.nblk) * (rank + 1) / p.cluster);
   }
 
-  // The warp's blocks are v0 + warp, v0 + warp + kWarps, ... Lane l keeps the page and the offset
-  // in it of the 16 tokens (l % 2) of the block l / 2 after the last look-up: 16 blocks at a time.
+  // The warp's blocks are v0 + warp, v0 + warp + kWarps, ... A block comes as `per` pieces of `unit`
+  // tokens, each within a page. Lane l keeps the page and the offset in it of the piece l % 4 of the
+  // block l / 4 after the last look-up: 8 blocks at a time.
   const int nmine = ok ? max(0, (v1 - v0 - warp + kWarps - 1) / kWarps) : 0;
   const int32_t* table = p.table + b * p.table_stride;
+  const int per = kBlk / unit;
   PageAt at{-1, 0};
-  uint32_t seen = 0;  // two bits per stage: which halves of the block have a page
-  // Copies of a block: lane 4 h + k brings, of its half h, the V rows (k = 0), the sign rows, mu or
+  uint32_t seen = 0;  // four bits per stage: which quarters of the block have a page
+  // Copies of a block: lane 4 i + k brings, of its piece i, the V rows (k = 0), the sign rows, mu or
   // the exponents, which lie at off + offset * size in the page's block.
-  const int half = (lane >> 2) & 1, kind = lane & 3;
+  const int piece = (lane >> 2) & 3, kind = lane & 3;
   const int xoff = kind == 1 ? cv.off_bits() : (kind == 2 ? cv.off_mu() : cv.off_exp());
   const int xsize = kind == 1 ? 16 : (kind == 2 ? 2 : 1);
-  const int xdst = (kind == 1 ? 0 : (kind == 2 ? S::xMu : S::xExp)) + kPageUnit * half * xsize;
+  const int xdst = (kind == 1 ? 0 : (kind == 2 ? S::xMu : S::xExp)) + unit * piece * xsize;
   auto issue = [&](int n, int to) {  // block n of the warp into stage `to`
     if (n >= nmine) return;
-    if ((n & 15) == 0) {
+    if ((n & 7) == 0) {
       at.page = -1;
-      const int m = n + (lane >> 1);
-      if (m < nmine) at = page_at(p, table, w.kv, w.block_at(v0 + warp + m * kWarps) * kBlk + (lane & 1) * kPageUnit);
+      const int m = n + (lane >> 2);
+      if (m < nmine && (lane & 3) < per)
+        at = page_at(p, table, w.kv, w.block_at(v0 + warp + m * kWarps) * kBlk + (lane & 3) * unit);
     }
-    const int page = __shfl_sync(0xffffffffu, at.page, 2 * (n & 15) + half);
-    const int off = __shfl_sync(0xffffffffu, at.off, 2 * (n & 15) + half);
-    // Bit 4 h of the vote: the half h has a page.
-    const uint32_t vote = __ballot_sync(0xffffffffu, page >= 0);
-    const uint32_t have = (vote & 1u) | ((vote >> 3) & 2u);
+    const int page = __shfl_sync(0xffffffffu, at.page, 4 * (n & 7) + piece);
+    const int off = __shfl_sync(0xffffffffu, at.off, 4 * (n & 7) + piece);
+    // Bits 0, 4, 8 and 12 of the vote: the pieces with a page.
+    const uint32_t vote = __ballot_sync(0xffffffffu, page >= 0 && lane < 16) & 0x1111u;
     const uint32_t bar = smem_u32(&s_full[warp][to]), extra = xring + to * S::kX + xdst;
-    if (lane == 0) mbar_arrive_expect_tx(&s_full[warp][to], ((have & 1u) + (have >> 1)) * S::kHalf);
+    if (lane == 0) mbar_arrive_expect_tx(&s_full[warp][to], __popc(vote) * unit * S::kToken);
     __syncwarp();
-    if (lane < 8) {
+    if (lane < 4 * per) {
       if (page < 0) {
         // No page: the rows are not seen, but what their scores are made of stays finite.
         if (kind > 0)
-          for (int i = 0; i < xsize; ++i) sts128(extra + 16 * i, 0u, 0u, 0u, 0u);
+          for (int i = 0; i < unit / 16 * xsize; ++i) sts128(extra + 16 * i, 0u, 0u, 0u, 0u);
       } else if (kind == 0) {
-        tma_load_3d(vring + to * S::kV + kPageUnit * half * S::kRow, &v_map, bar, 0, off, page * cv.heads + head);
+        tma_load_3d(vring + to * S::kV + unit * piece * S::kRow, &v_map, bar, 0, off, page * cv.heads + head);
       } else {
-        bulk_load(extra, cv.block(page, head) + xoff + off * xsize, kPageUnit * xsize, bar);
+        bulk_load(extra, cv.block(page, head) + xoff + off * xsize, unit * xsize, bar);
       }
     }
-    seen = (seen & ~(3u << (2 * to))) | (have << (2 * to));
+    // Per quarter: of one piece (all four), two (two each) or four.
+    const uint32_t have = per == 4 ? (vote * 0x1248u >> 12) & 15u : (per == 2 ? (vote & 1u) * 3u + (vote >> 4 & 1u) * 12u : vote * 15u);
+    seen = (seen & ~(15u << (4 * to))) | (have << (4 * to));
   };
 #pragma unroll
   for (int n = 0; n < kStages; ++n) issue(n, st + n >= kStages ? st + n - kStages : st + n);
@@ -382,23 +393,34 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 3)
     ok = __all_sync(0xffffffffu, wait_stage(&s_full[warp][st], (phase >> st) & 1u));
     if (!ok) break;
     phase ^= 1u << st;
-    const uint32_t have = (seen >> (2 * st)) & 3u;
-    uint32_t word[2][2];
+    const uint32_t have = (seen >> (4 * st)) & 15u;
+    // The block's sign words, before floats take their place.
+    uint32_t word[kQ][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < kQ; ++h)
 #pragma unroll
       for (int k = 0; k < 2; ++k) word[h][k] = lds32(fl + (16 * h + key0 + 2 * k) * 16 + 4 * t);
     {
-      const int e = static_cast<int8_t>(lds16(fl + S::xExp + (lane & ~1)) >> (8 * (lane & 1)));
-      const int ec = min(max(e, kMinExp), kMaxExp);
-      const uint32_t mu = lds16(fl + S::xMu + 2 * lane) << 16;
-      __syncwarp();
-      sts128(fl + 16 * lane, mu, __float_as_uint(static_cast<float>(ec)), static_cast<uint32_t>(127 - ec) << 23, 0u);
-    }
-    // 64 sum q k of 16 keys each (h) and 8 rows.
-    int x[NR][2][4];
+      uint32_t mu[kBlk / 32];
+      int e[kBlk / 32];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+      for (int i = 0; i < kBlk / 32; ++i) {
+        const int j = 32 * i + lane;
+        e[i] = min(max(static_cast<int>(static_cast<int8_t>(lds16(fl + S::xExp + (j & ~1)) >> (8 * (lane & 1)))), kMinExp), kMaxExp);
+        mu[i] = lds16(fl + S::xMu + 2 * j) << 16;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kBlk / 32; ++i)
+        sts128(fl + 16 * (32 * i + lane), mu[i], __float_as_uint(static_cast<float>(e[i])),
+               static_cast<uint32_t>(127 - e[i]) << 23, 0u);
+      __syncwarp();
+    }
+    // Scores + e of the keys 16 h + key0 + 2 k and the rows 2 t and 2 t + 1.
+    float2 sc[NR][kQ][2];
+#pragma unroll
+    for (int h = 0; h < kQ; ++h) {
+      int x[NR][4];  // 64 sum q k of 16 keys and 8 rows
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         const uint32_t a0 = word[h][0] & (0x01010101u << (2 * s)), a1 = word[h][1] & (0x01010101u << (2 * s));
@@ -407,35 +429,30 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 3)
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           if (s == 0)
-            mma_qk_first(x[r][h], start, a0, a1, a2, a3, qb[r][0], qb[r][1]);
+            mma_qk_first(x[r], start, a0, a1, a2, a3, qb[r][0], qb[r][1]);
           else
-            mma_qk(x[r][h], a0, a1, a2, a3, qb[r][2 * s], qb[r][2 * s + 1]);
+            mma_qk(x[r], a0, a1, a2, a3, qb[r][2 * s], qb[r][2 * s + 1]);
         }
       }
-    __syncwarp();
-    // Scores + e of the key 16 h + key0 + 2 k and the rows 2 t and 2 t + 1.
-    float2 sc[NR][2][2];
-    float down[2][2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const float4 f = lds_f4(fl + (16 * h + key0 + 2 * k) * 16);
-        down[h][k] = f.z;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           // x = sum q - 2 sum q k: exact, the constant of the accumulator's start taken off with it.
-          float2 y = __ffma2_rn(make_float2(__int_as_float(x[r][h][2 * k]), __int_as_float(x[r][h][2 * k + 1])),
+          float2 y = __ffma2_rn(make_float2(__int_as_float(x[r][2 * k]), __int_as_float(x[r][2 * k + 1])),
                                 make_float2(-0.03125f, -0.03125f), back[r]);
           y = __fmul2_rn(y, cq[r]);
           sc[r][h][k] = make_float2(__fmaf_rn(y.x, f.x, f.y), __fmaf_rn(y.y, f.x, f.y));
         }
       }
-    if (!(have == 3u && j0 + kBlk - 1 <= all_last && j0 >= all_lo)) {
+    }
+    if (!(have == 15u && j0 + kBlk - 1 <= all_last && j0 >= all_lo)) {
+      __syncwarp();  // keeps this a branch: most blocks need no mask
 #pragma unroll
       for (int r = 0; r < NR; ++r)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < kQ; ++h)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int j = j0 + 16 * h + key0 + 2 * k;
@@ -444,12 +461,16 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 3)
             if (!(in && j <= last[r][1] && (j >= wlo[r][1] || sink))) sc[r][h][k].y = -CUDART_INF_F;
           }
     }
-    uint32_t bw[NR][2][2];  // weights of row g: high and low bytes of the keys 16 h + 4 t .. + 3
-    float2 f2[NR];          // what they count, for the rows 2 t and 2 t + 1
+    uint32_t bw[NR][2][kQ];  // weights of row g: high and low bytes of the keys 16 h + 4 t .. + 3
+    float2 f2[NR];           // what they count, for the rows 2 t and 2 t + 1
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      float2 mx = make_float2(fmaxf(fmaxf(sc[r][0][0].x, sc[r][0][1].x), fmaxf(sc[r][1][0].x, sc[r][1][1].x)),
-                              fmaxf(fmaxf(sc[r][0][0].y, sc[r][0][1].y), fmaxf(sc[r][1][0].y, sc[r][1][1].y)));
+      float2 mx = make_float2(fmaxf(sc[r][0][0].x, sc[r][0][1].x), fmaxf(sc[r][0][0].y, sc[r][0][1].y));
+#pragma unroll
+      for (int h = 1; h < kQ; ++h) {
+        mx.x = fmax3(mx.x, sc[r][h][0].x, sc[r][h][1].x);
+        mx.y = fmax3(mx.y, sc[r][h][0].y, sc[r][h][1].y);
+      }
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
         mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, o));
@@ -475,14 +496,15 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 3)
                                    mx.y == -CUDART_INF_F ? 0.0f : ex2(mx.y - M[r].y));
       float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kQ; ++h) {
         uint32_t w16[2];  // 16-bit weights of the keys 16 h + 4 t + 2 k and the next, of row g
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float2 y = __fadd2_rn(sc[r][h][k], ref);
           const float2 e = make_float2(ex2(y.x), ex2(y.y));
-          sum.x = __fmaf_rn(e.x, down[h][k], sum.x);
-          sum.y = __fmaf_rn(e.y, down[h][k], sum.y);
+          const float down = __uint_as_float(lds32(fl + (16 * h + key0 + 2 * k) * 16 + 8));  // 2^-e
+          sum.x = __fmaf_rn(e.x, down, sum.x);
+          sum.y = __fmaf_rn(e.y, down, sum.y);
           const float2 z = __ffma2_rn(e, make_float2(kUnit, kUnit), make_float2(kMagic, kMagic));
           w16[k] = turn8(__byte_perm(__float_as_uint(z.x), __float_as_uint(z.y), 0x5410));
         }
@@ -495,13 +517,16 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 3)
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       if (16 * m < dp) {
-        uint32_t a[4];  // channels g and g + 8 of the tile: keys 4 t .. + 3 of the block's halves
-        ldmatrix_t8((vbase + stage) ^ (m * 16), a);
+        uint32_t a[2][4];  // channels g and g + 8 of the tile: keys 4 t .. + 3 of two quarters each
+        ldmatrix_t8((vbase + stage) ^ (m * 16), a[0]);
+        ldmatrix_t8((vbase + stage + 32 * S::kRow) ^ (m * 16), a[1]);
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           int hi[4], lo[4];
-          mma_pv(hi, start, a[0], a[1], a[2], a[3], bw[r][0][0], bw[r][0][1]);
-          mma_pv(lo, start, a[0], a[1], a[2], a[3], bw[r][1][0], bw[r][1][1]);
+          mma_pv_first(hi, start, a[0], bw[r][0][0], bw[r][0][1]);
+          mma_pv_first(lo, start, a[0], bw[r][1][0], bw[r][1][1]);
+          mma_pv(hi, a[1], bw[r][0][2], bw[r][0][3]);
+          mma_pv(lo, a[1], bw[r][1][2], bw[r][1][3]);
 #pragma unroll
           for (int i = 0; i < 4; i += 2) {
             float2 o = make_float2(acc[r][m][i], acc[r][m][i + 1]);
@@ -723,16 +748,18 @@ cudaError_t launch_decode(const PagedAttnParams& p, int dt, cudaStream_t s) {
   constexpr int smem = Ring<CPG>::total(8 * NR);
   cudaError_t e = allow_smem<paged_decode_kernel<CPG, NR>>(smem);
   if (e != cudaSuccess) return e;
-  // The V rows of all blocks, as (byte, token, block); a copy brings 16 rows, padded to CPG * 8 bytes.
+  // The V rows of all blocks, as (byte, token, block); a copy brings `unit` rows of a page, padded to
+  // CPG * 8 bytes.
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return cudaErrorNotSupported;
   const CacheView& cv = p.cache;
+  const int unit = cv.page_size % 64 == 0 ? 64 : (cv.page_size % 32 == 0 ? 32 : 16);
   CUtensorMap map{};
   if (cv.num_pages > 0) {
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cv.dp), static_cast<cuuint64_t>(cv.page_size),
                                 static_cast<cuuint64_t>(cv.num_pages) * cv.heads};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cv.dp), static_cast<cuuint64_t>(cv.block_bytes)};
-    const cuuint32_t box[3] = {CPG * 8, kPageUnit, 1}, step[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {CPG * 8, static_cast<cuuint32_t>(unit), 1}, step[3] = {1, 1, 1};
     if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, cv.data, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CPG == 16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -752,7 +779,7 @@ cudaError_t launch_decode(const PagedAttnParams& p, int dt, cudaStream_t s) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.numAttrs = 1;
   }
-  e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<CPG, NR>, p, dt == BA_F16 ? 1 : 0, map);
+  e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<CPG, NR>, p, dt == BA_F16 ? 1 : 0, unit, map);
   if (e != cudaSuccess || p.ctas == 0) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(p.ctas * p.row_tile));
   cfg.dynamicSmemBytes = 0;
@@ -789,7 +816,7 @@ void paged_decode_plan(PagedAttnParams* p, int sms) {
     keys = std::min<int64_t>(keys, static_cast<int64_t>(p->window) + p->row_tile + p->sinks + 2 * kBlk);
   const int64_t blocks = std::max<int64_t>(1, ceil_div(keys, kBlk));
   const int64_t tiles = static_cast<int64_t>(p->B) * p->row_tiles * p->cache.heads;
-  const int64_t fit = static_cast<int64_t>(sms) * (p->row_tile == 8 ? 4 : 3);  // CTAs at once, by registers
+  const int64_t fit = static_cast<int64_t>(sms) * 3;  // CTAs at once, by registers and shared memory
   // Short contexts: a cluster of up to eight CTAs per (tile, head), down to a block per warp, joins
   // its parts itself. Where that leaves a warp more than kShort blocks beyond its share of an even
   // split over the GPU (or more than kShort of them, when the CTAs do not fit at once and ragged
