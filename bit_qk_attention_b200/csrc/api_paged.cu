@@ -99,6 +99,10 @@ ba_status plan(const ba_kv_cache* cache, const ba_paged_seqs* s, PagedAttnParams
   const int64_t tiles = ceil_div(rows, p->row_tile);
   if (tiles > kMaxCtas / (static_cast<int64_t>(p->B) * p->cache.heads)) return BA_ERR_UNSUPPORTED;
   p->row_tiles = static_cast<int>(tiles);
+  p->by_group = FastDiv::of(p->group);
+  p->by_kv_heads = FastDiv::of(p->cache.heads);
+  p->by_page = FastDiv::of(p->cache.page_size);
+  p->by_tiles = FastDiv::of(p->row_tiles);
   if (tiles * p->B * p->cache.heads > kMaxCtas / p->row_tile) return BA_ERR_UNSUPPORTED;
   p->nsplit = 1;
   if (p->row_tile == 256) {

@@ -171,18 +171,9 @@ __device__ __forceinline__ float lds_cluster(uint32_t a, int rank) {
   return x;
 }
 
-// One row of q by a warp: sign words and sum of |x|.
-template <typename T>
-__device__ __forceinline__ void scan_row(const T* src, int d, int lane, uint32_t (&word)[4], float& sum) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int c = 32 * k + lane;
-    const float x = c < d ? load1<T>(src + c) : 0.0f;
-    word[k] = __ballot_sync(0xffffffffu, x < 0.0f);
-    sum += fabsf(x);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+// A 16-bit number, widened.
+__device__ __forceinline__ float widen(uint16_t x, int f16) {
+  return f16 ? __half2float(__ushort_as_half(x)) : __uint_as_float(static_cast<uint32_t>(x) << 16);
 }
 
 template <int CPG, int NR>
@@ -200,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   auto s_mu = reinterpret_cast<float*>(smem + oMu);
 
   allow_dependents();
+  grid_dependency_wait();
   const CacheView& cv = p.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int dp = cv.dp;
@@ -222,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       return;
     }
   } else {
-    line.entry = blockIdx.x / p.cluster / cv.heads;
+    line.entry = p.by_kv_heads(blockIdx.x / p.cluster);
   }
 
   // One (tile, head) per cluster: its CTAs take equal parts and join them through their shared memory.
@@ -231,8 +223,8 @@ __global__ void __launch_bounds__(kThreads, 3)
   for (bool more = true; more;) {
   // The next (tile, head) of the CTA: its blocks v0 .. v1 - 1 of all.
   const RowTile w = entry_tile(p, line.entry, kBlk);
-  const int b = line.entry / p.row_tiles;
-  int head = blockIdx.x / p.cluster % cv.heads, v0 = 0, v1 = w.nblk, slot = -1;  // slot -1: nothing is cut
+  const int b = p.by_tiles(line.entry);
+  int head = blockIdx.x / p.cluster - line.entry * cv.heads, v0 = 0, v1 = w.nblk, slot = -1;  // slot -1: nothing is cut
   if (p.ctas > 0) {
     const int units = units_of(w, kCost);
     if (units == 0) {  // a tile without rows
@@ -241,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
     const int entry = line.entry;
     const int64_t in = line.at - line.base;
-    head = static_cast<int>(in / units);
+    head = (in >> 32) == 0 ? static_cast<uint32_t>(in) / static_cast<uint32_t>(units) : static_cast<int>(in / units);
     const int u0 = static_cast<int>(in - static_cast<int64_t>(head) * units);
     const int u1 = static_cast<int>(min(static_cast<int64_t>(units), u0 + line.end - line.at));
     const int64_t stop = line.at + (units - u0);  // where the (tile, head) ends
@@ -261,8 +253,23 @@ __global__ void __launch_bounds__(kThreads, 3)
   } else {
     more = false;
     if (w.rows <= 0) return;
-    v0 = static_cast<int>(static_cast<int64_t>(w.nblk) * rank / p.cluster);
-    v1 = static_cast<int>(static_cast<int64_t>(w.nblk) * (rank + 1) / p.cluster);
+    v0 = w.nblk * rank / p.cluster;  // a power of two below 16; nblk < 2^23
+    v1 = w.nblk * (rank + 1) / p.cluster;
+  }
+
+  // The rows of q are asked for first; their signs are taken while the first blocks are on their way.
+  constexpr int QR = R / kWarps;
+  uint16_t q_raw[QR][4];
+#pragma unroll
+  for (int u = 0; u < QR; ++u) {
+    const int r = warp + u * kWarps, i = p.by_group(w.r0 + r);
+    const uint16_t* src = static_cast<const uint16_t*>(p.q) + (w.t0 + i) * p.q_stride_t +
+                          (head * p.group + w.r0 + r - i * p.group) * p.q_stride_h;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      q_raw[u][k] = 0;
+      if (32 * k < CH && r < w.rows && 32 * k + lane < cv.d) q_raw[u][k] = __ldg(src + 32 * k + lane);
+    }
   }
 
   // The warp's blocks are v0 + warp, v0 + warp + kWarps, ... A block comes as `per` pieces of `unit`
@@ -312,18 +319,20 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
   for (int n = 0; n < kStages; ++n) issue(n, st + n >= kStages ? st + n - kStages : st + n);
 
-  // Sign bits and scale of the rows, while the first blocks are on their way.
-  for (int r = warp; r < R; r += kWarps) {
-    uint32_t word[4] = {0u, 0u, 0u, 0u};
+  // Sign words and scales of the rows.
+#pragma unroll
+  for (int u = 0; u < QR; ++u) {
+    uint32_t word[4];
     float sum = 0.0f;
-    if (r < w.rows) {
-      const int i = (w.r0 + r) / p.group, hq = head * p.group + (w.r0 + r) % p.group;
-      const int64_t src = (w.t0 + i) * p.q_stride_t + hq * p.q_stride_h;
-      if (q_f16)
-        scan_row(static_cast<const __half*>(p.q) + src, cv.d, lane, word, sum);
-      else
-        scan_row(static_cast<const __nv_bfloat16*>(p.q) + src, cv.d, lane, word, sum);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float x = widen(q_raw[u][k], q_f16);
+      word[k] = __ballot_sync(0xffffffffu, x < 0.0f);
+      sum += fabsf(x);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int r = warp + u * kWarps;
     if (lane < 4) s_bits[r][lane] = lane == 0 ? word[0] : (lane == 1 ? word[1] : (lane == 2 ? word[2] : word[3]));
     if (lane == 0) s_mu[r] = sum / static_cast<float>(cv.d);
   }
@@ -354,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       const int neg = __popc(s_bits[r][0]) + __popc(s_bits[r][1]) + __popc(s_bits[r][2]) + __popc(s_bits[r][3]);
       b2[i] = static_cast<float>(cv.d - 2 * neg) + kMagic / 32.0f;
       c2[i] = p.scale_log2 * s_mu[r];
-      const int pos = w.pos0() + (w.r0 + r) / p.group;
+      const int pos = w.pos0() + p.by_group(w.r0 + r);
       last[n][i] = r < w.rows ? (p.causal ? min(pos, w.kv - 1) : w.kv - 1) : -1;
       wlo[n][i] = p.causal && p.window > 0 ? pos - p.window + 1 : 0;
     }
@@ -362,8 +371,8 @@ __global__ void __launch_bounds__(kThreads, 3)
     back[n] = make_float2(b2[0], b2[1]);
   }
   // What every row of the tile sees: keys <= all_last from all_lo on.
-  const int all_last = p.causal ? min(w.pos0() + w.r0 / p.group, w.kv - 1) : w.kv - 1;
-  const int all_lo = p.causal && p.window > 0 ? w.pos0() + (w.r0 + w.rows - 1) / p.group - p.window + 1 : 0;
+  const int all_last = p.causal ? min(w.pos0() + p.by_group(w.r0), w.kv - 1) : w.kv - 1;
+  const int all_lo = p.causal && p.window > 0 ? w.pos0() + p.by_group(w.r0 + w.rows - 1) - p.window + 1 : 0;
 
   float acc[NR][MT][4];
   float2 M[NR], l[NR];  // of the rows 2 t and 2 t + 1
@@ -583,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       f[k] = s_ml[k][r].x == -CUDART_INF_F ? 0.0f : ex2(s_ml[k][r].x - Mr);
       lr += f[k] * s_ml[k][r].y;
     }
-    const int64_t row = (w.t0 + (w.r0 + r) / p.group) * p.heads + head * p.group + (w.r0 + r) % p.group;
+    const int64_t row = out_row(p, w, head, r);
     const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * R + r;
     const float inv = lr > 0.0f ? 1.0f / lr : 0.0f;
     for (int c = lane; c < dp; c += 32) {
@@ -611,23 +620,34 @@ __global__ void __launch_bounds__(kThreads, 3)
     cluster_arrive();
     cluster_wait();
     for (int r = rank + p.cluster * warp; r < w.rows; r += p.cluster * kWarps) {
-      float Mr = -CUDART_INF_F, lr = 0.0f, x[CH / 32];
+      // Lane k has the (M, l) of part k.
+      const bool is = lane < p.cluster;
+      const float Mk = is ? lds_cluster(smem_u32(&s_fin[r]), lane) : -CUDART_INF_F;
+      const float lk = is ? lds_cluster(smem_u32(&s_fin[r]) + 4, lane) : 0.0f;
+      float x[8][CH / 32];
 #pragma unroll
-      for (int i = 0; i < CH / 32; ++i) x[i] = 0.0f;
-      for (int k = 0; k < p.cluster; ++k) Mr = fmaxf(Mr, lds_cluster(smem_u32(&s_fin[r]), k));
-      for (int k = 0; k < p.cluster; ++k) {
-        const float Mk = lds_cluster(smem_u32(&s_fin[r]), k);
-        const float f = Mk == -CUDART_INF_F ? 0.0f : ex2(Mk - Mr);
-        lr = __fmaf_rn(f, lds_cluster(smem_u32(&s_fin[r]) + 4, k), lr);
+      for (int k = 0; k < 8; ++k)
 #pragma unroll
         for (int i = 0; i < CH / 32; ++i)
-          x[i] = __fmaf_rn(f, lds_cluster(smem_u32(&s_sum[r * CH + 32 * i + lane]), k), x[i]);
-      }
-      const int64_t row = (w.t0 + (w.r0 + r) / p.group) * p.heads + head * p.group + (w.r0 + r) % p.group;
-      const float inv = lr > 0.0f ? 1.0f / lr : 0.0f;
+          x[k][i] = k < p.cluster ? lds_cluster(smem_u32(&s_sum[r * CH + 32 * i + lane]), k) : 0.0f;
+      float Mr = Mk;
 #pragma unroll
-      for (int i = 0; i < CH / 32; ++i)
-        if (32 * i + lane < cv.d) store_out(p.o, row * cv.d + 32 * i + lane, x[i] * inv, p.o_dt);
+      for (int o = 4; o > 0; o >>= 1) Mr = fmaxf(Mr, __shfl_xor_sync(0xffffffffu, Mr, o));
+      const float f = Mk == -CUDART_INF_F ? 0.0f : ex2(Mk - Mr);
+      float lr = f * lk;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) lr += __shfl_xor_sync(0xffffffffu, lr, o);
+      Mr = __shfl_sync(0xffffffffu, Mr, 0);
+      lr = __shfl_sync(0xffffffffu, lr, 0);
+      const float inv = lr > 0.0f ? 1.0f / lr : 0.0f;
+      const int64_t row = out_row(p, w, head, r);
+#pragma unroll
+      for (int i = 0; i < CH / 32; ++i) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum = __fmaf_rn(__shfl_sync(0xffffffffu, f, k), x[k][i], sum);
+        if (32 * i + lane < cv.d) store_out(p.o, row * cv.d + 32 * i + lane, sum * inv, p.o_dt);
+      }
       if (lane == 0 && p.lse != nullptr) p.lse[row] = lr > 0.0f ? (Mr + log2f(lr)) * CUDART_LN2_F : -CUDART_INF_F;
     }
     // No CTA leaves while another reads its shared memory.
@@ -684,7 +704,7 @@ __global__ void __launch_bounds__(kThreads) line_join_kernel(PagedAttnParams p, 
   if (lane == 0) s_l[warp] = l;
   __syncthreads();
   const float lt = s_l[0] + s_l[1] + s_l[2] + s_l[3];
-  const int64_t row = (w.t0 + (w.r0 + r) / p.group) * p.heads + note.head * p.group + (w.r0 + r) % p.group;
+  const int64_t row = out_row(p, w, note.head, r);
   const int c = threadIdx.x;
   if (c < cv.d) {
     const float sum = s_x[0][c] + s_x[1][c] + s_x[2][c] + s_x[3][c];
@@ -767,25 +787,26 @@ cudaError_t launch_decode(const PagedAttnParams& p, int dt, cudaStream_t s) {
   }
   const int64_t tiles = static_cast<int64_t>(p.B) * p.row_tiles * cv.heads;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(static_cast<unsigned>(p.ctas > 0 ? p.ctas : tiles * p.cluster));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
+  // Its launch overlaps the end of the kernel before it; it waits for that one before it reads anything.
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
   if (p.ctas == 0 && p.cluster > 1) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = p.cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.numAttrs = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
   }
   e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<CPG, NR>, p, dt == BA_F16 ? 1 : 0, unit, map);
   if (e != cudaSuccess || p.ctas == 0) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(p.ctas * p.row_tile));
   cfg.dynamicSmemBytes = 0;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, line_join_kernel, p, kBlk);
 }
 

@@ -40,6 +40,20 @@ struct CacheReadParams {
   void* v;
 };
 
+// n / d for 0 <= n < 2^31, without a division: mul = ceil(2^(31 + s) / d) with 2^(s-1) < d <= 2^s is
+// off by less than 2^s / 2^(31 + s) of the quotient's scale, too little to reach the next whole number.
+struct FastDiv {
+  uint32_t mul, shift;
+  static FastDiv of(int d) {
+    uint32_t s = 0;
+    while ((int64_t{1} << s) < d) ++s;
+    return {static_cast<uint32_t>(((uint64_t{1} << (31 + s)) + d - 1) / d), 31 + s};
+  }
+  __host__ __device__ int operator()(int n) const {
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> shift);
+  }
+};
+
 // Attention of new tokens over the cache.
 struct JoinNote;
 struct PagedAttnParams {
@@ -47,6 +61,7 @@ struct PagedAttnParams {
   const void* q;
   int64_t q_stride_t, q_stride_h;  // elements
   int B, heads, group;             // group = query heads per KV head
+  FastDiv by_group, by_kv_heads, by_page, by_tiles;  // divide by group, KV heads, page size, row tiles
   int64_t T;
   int max_q_len, max_kv_len;  // max_kv_len also within the page table
   const int32_t* cu;          // null: one row per sequence
@@ -99,8 +114,8 @@ __device__ __forceinline__ RowTile row_tile(const PagedAttnParams& p, int b, int
                                 static_cast<int64_t>(min(w.nq, p.max_q_len)) * p.group - w.r0));
   int lo = 0, hi = w.kv;
   if (p.causal && w.rows > 0) {
-    hi = min(hi, w.pos0() + (w.r0 + w.rows - 1) / p.group + 1);
-    if (p.window > 0) lo = max(0, w.pos0() + w.r0 / p.group - p.window + 1);
+    hi = min(hi, w.pos0() + p.by_group(w.r0 + w.rows - 1) + 1);
+    if (p.window > 0) lo = max(0, w.pos0() + p.by_group(w.r0) - p.window + 1);
   }
   w.first = lo / bk;
   w.nsink = min(static_cast<int>(ceil_div(p.sinks, bk)), w.first);
@@ -114,13 +129,19 @@ __device__ __forceinline__ RowTile row_tile(const PagedAttnParams& p, int b, int
 // may be cut at the ends of CTAs. What a CTA computes of a cut one goes into the workspace: slot 0 if
 // it began before the CTA, else slot 1. The CTA in which a cut one begins leaves a note for the
 // kernel that joins the parts.
+// Row of o (and of lse) of the tile's row r.
+__device__ __forceinline__ int64_t out_row(const PagedAttnParams& p, const RowTile& w, int head, int r) {
+  const int i = p.by_group(w.r0 + r);
+  return (w.t0 + i) * p.heads + head * p.group + (w.r0 + r - i * p.group);
+}
+
 struct JoinNote {
   int entry, head;  // entry = b * row_tiles + tile
   int last;         // CTA with the last part; the CTAs between have it in slot 0. -1: nothing to join
 };
 
 __device__ __forceinline__ RowTile entry_tile(const PagedAttnParams& p, int entry, int bk) {
-  const int b = entry / p.row_tiles;
+  const int b = p.by_tiles(entry);
   return row_tile(p, b, entry - b * p.row_tiles, bk);
 }
 
@@ -160,7 +181,9 @@ __device__ __forceinline__ Stretch find_stretch(const PagedAttnParams& p, int bk
   }
   total *= heads;
   Stretch st;
-  st.per = static_cast<int>(max(ceil_div(total, gridDim.x), static_cast<int64_t>(min_units)));
+  st.per = max(min_units, static_cast<int>((total >> 32) == 0
+                                               ? (static_cast<uint32_t>(total) + gridDim.x - 1) / gridDim.x
+                                               : ceil_div(total, gridDim.x)));
   st.at = static_cast<int64_t>(blockIdx.x) * st.per;
   st.end = min(total, st.at + st.per);
   int64_t base = before * heads;
@@ -194,7 +217,7 @@ struct PageAt {
 __device__ __forceinline__ PageAt page_at(const PagedAttnParams& p, const int32_t* table, int kv, int j) {
   PageAt at{-1, 0};
   if (j < kv) {
-    const int e = j / p.cache.page_size;
+    const int e = p.by_page(j);
     at.page = table[e];
     at.off = j - e * p.cache.page_size;
     if (at.page < 0 || at.page >= p.cache.num_pages) at.page = -1;
@@ -207,10 +230,10 @@ __device__ __forceinline__ void cta_of(const PagedAttnParams& p, unsigned idx, i
                                        int& part) {
   part = idx % n;
   idx /= n;
-  head = idx % p.cache.heads;
-  idx /= p.cache.heads;
-  tile = idx % p.row_tiles;
-  b = idx / p.row_tiles;
+  const int i = p.by_kv_heads(idx);
+  head = idx - i * p.cache.heads;
+  b = p.by_tiles(i);
+  tile = i - b * p.row_tiles;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
