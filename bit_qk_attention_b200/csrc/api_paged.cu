@@ -104,20 +104,11 @@ ba_status plan(const ba_kv_cache* cache, const ba_paged_seqs* s, PagedAttnParams
   p->by_page = FastDiv::of(p->cache.page_size);
   p->by_tiles = FastDiv::of(p->row_tiles);
   if (tiles * p->B * p->cache.heads > kMaxCtas / p->row_tile) return BA_ERR_UNSUPPORTED;
-  p->nsplit = 1;
-  if (p->row_tile == 256) {
-    int blocks = 0;
-    p->split_blocks = paged_chunk_split_blocks(*p, sm_count(), &blocks);
-    p->nsplit = std::max(1, static_cast<int>(ceil_div(blocks, p->split_blocks)));
-    if (tiles * p->B * p->cache.heads > kMaxCtas / p->nsplit) return BA_ERR_UNSUPPORTED;
-    if (p->nsplit > 1) {
-      const size_t n = static_cast<size_t>(p->nsplit) * p->T * p->heads;
-      *ws = align_up(n * p->cache.dp * 4) + align_up(n * 8);
-    }
-  } else {
+  if (p->row_tile == 256)
+    paged_chunk_plan(p, sm_count());
+  else
     paged_decode_plan(p, sm_count());
-    if (p->ctas > 0) *ws = line_workspace(*p, nullptr);
-  }
+  if (p->ctas > 0) *ws = line_workspace(*p, nullptr);
   return BA_OK;
 }
 
@@ -198,11 +189,7 @@ ba_status ba_attention_paged(const void* q, int64_t q_stride_t, int64_t q_stride
     if (ws == nullptr || ws_bytes < need) return BA_ERR_WORKSPACE;
     if (!aligned(ws, 16)) return BA_ERR_ALIGNMENT;
     p.part_o = static_cast<float*>(ws);
-    const size_t n = static_cast<size_t>(p.nsplit) * p.T * p.heads;
-    if (p.ctas > 0)
-      line_workspace(p, &p);
-    else
-      p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + align_up(n * p.cache.dp * 4));
+    line_workspace(p, &p);
   }
   p.q = q;
   p.q_stride_t = q_stride_t;

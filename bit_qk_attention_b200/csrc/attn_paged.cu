@@ -661,105 +661,59 @@ __global__ void __launch_bounds__(kThreads, 3)
 }
 
 // Joins the parts of a (tile, head) that the line of units cut: o = sum_k 2^(M_k - M) o_k / sum_k
-// 2^(M_k - M) l_k. One CTA per CTA of the first kernel and row of a tile; its warps take every fourth
-// part, four channels per lane, and meet in shared memory.
-__global__ void __launch_bounds__(kThreads) line_join_kernel(PagedAttnParams p, int bk) {
-  __shared__ float s_x[kWarps][128];
-  __shared__ float s_l[kWarps];
+// 2^(M_k - M) l_k. A CTA takes `rows` rows of what one CTA of the first kernel left a note of, one after
+// the other; of a row its warps take every fourth part, four channels per lane, and meet in shared
+// memory.
+__global__ void __launch_bounds__(kThreads) line_join_kernel(PagedAttnParams p, int bk, int rows) {
+  __shared__ float s_x[2][kWarps][128];
+  __shared__ float s_l[2][kWarps];
   const CacheView& cv = p.cache;
-  const int cta = blockIdx.x % p.ctas, r = blockIdx.x / p.ctas;
+  const int cta = blockIdx.x % p.ctas, r0 = blockIdx.x / p.ctas * rows;
   // Every CTA waits, also one with nothing to join: this grid must not complete before the one
   // whose parts it joins.
   grid_dependency_wait();
   const JoinNote note = p.notes[cta];
   if (note.last < 0) return;
   const RowTile w = entry_tile(p, note.entry, bk);
-  if (r >= w.rows) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = note.last - cta + 1;
-  // Part k: slot 1 of the first CTA, slot 0 of the others.
-  auto part = [&](int k) { return (static_cast<int64_t>(cta + k) * 2 + (k == 0 ? 1 : 0)) * p.row_tile + r; };
-  float M = -CUDART_INF_F;
-  for (int k = lane; k < n; k += 32) M = fmaxf(M, p.part_ml[part(k)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float ref = M == -CUDART_INF_F ? 0.0f : M;
-  float l = 0.0f;
-  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   const bool on = 4 * lane < cv.dp;
+  for (int r = r0; r < min(r0 + rows, w.rows); ++r) {
+    // Part k: slot 1 of the first CTA, slot 0 of the others.
+    auto part = [&](int k) { return (static_cast<int64_t>(cta + k) * 2 + (k == 0 ? 1 : 0)) * p.row_tile + r; };
+    float M = -CUDART_INF_F;
+    for (int k = lane; k < n; k += 32) M = fmaxf(M, p.part_ml[part(k)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float ref = M == -CUDART_INF_F ? 0.0f : M;
+    float l = 0.0f;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
-  for (int k = warp; k < n; k += kWarps) {
-    const int64_t at = part(k);
-    const float2 ml = p.part_ml[at];
-    const float4 o = on ? *reinterpret_cast<const float4*>(p.part_o + at * cv.dp + 4 * lane)
-                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const float f = ex2(ml.x - ref);
-    l = __fmaf_rn(f, ml.y, l);
-    x.x = __fmaf_rn(f, o.x, x.x);
-    x.y = __fmaf_rn(f, o.y, x.y);
-    x.z = __fmaf_rn(f, o.z, x.z);
-    x.w = __fmaf_rn(f, o.w, x.w);
+    for (int k = warp; k < n; k += kWarps) {
+      const int64_t at = part(k);
+      const float2 ml = p.part_ml[at];
+      const float4 o = on ? *reinterpret_cast<const float4*>(p.part_o + at * cv.dp + 4 * lane)
+                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const float f = ex2(ml.x - ref);
+      l = __fmaf_rn(f, ml.y, l);
+      x.x = __fmaf_rn(f, o.x, x.x);
+      x.y = __fmaf_rn(f, o.y, x.y);
+      x.z = __fmaf_rn(f, o.z, x.z);
+      x.w = __fmaf_rn(f, o.w, x.w);
+    }
+    const int buf = r & 1;  // by turns, so that one barrier per row is enough
+    *reinterpret_cast<float4*>(&s_x[buf][warp][4 * lane]) = x;
+    if (lane == 0) s_l[buf][warp] = l;
+    __syncthreads();
+    const float lt = s_l[buf][0] + s_l[buf][1] + s_l[buf][2] + s_l[buf][3];
+    const int64_t row = out_row(p, w, note.head, r);
+    const int c = threadIdx.x;
+    if (c < cv.d) {
+      const float sum = s_x[buf][0][c] + s_x[buf][1][c] + s_x[buf][2][c] + s_x[buf][3][c];
+      store_out(p.o, row * cv.d + c, lt > 0.0f ? sum / lt : 0.0f, p.o_dt);
+    }
+    if (c == 0 && p.lse != nullptr) p.lse[row] = lt > 0.0f ? (M + log2f(lt)) * CUDART_LN2_F : -CUDART_INF_F;
   }
-  *reinterpret_cast<float4*>(&s_x[warp][4 * lane]) = x;
-  if (lane == 0) s_l[warp] = l;
-  __syncthreads();
-  const float lt = s_l[0] + s_l[1] + s_l[2] + s_l[3];
-  const int64_t row = out_row(p, w, note.head, r);
-  const int c = threadIdx.x;
-  if (c < cv.d) {
-    const float sum = s_x[0][c] + s_x[1][c] + s_x[2][c] + s_x[3][c];
-    store_out(p.o, row * cv.d + c, lt > 0.0f ? sum / lt : 0.0f, p.o_dt);
-  }
-  if (c == 0 && p.lse != nullptr) p.lse[row] = lt > 0.0f ? (M + log2f(lt)) * CUDART_LN2_F : -CUDART_INF_F;
-}
-
-// Joins the parts of each row: o = sum_k 2^(M_k - M) o_k / sum_k 2^(M_k - M) l_k. One CTA per row: its
-// warps take every fourth part, four channels per lane, and meet in shared memory.
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(PagedAttnParams p, int bk) {
-  __shared__ float s_x[kWarps][128];
-  __shared__ float s_l[kWarps];
-  const CacheView& cv = p.cache;
-  int b, tile, head, r;
-  cta_of(p, blockIdx.x, p.row_tile, b, tile, head, r);
-  // Every CTA waits, also one with nothing to join: this grid must not complete before the one
-  // whose parts it joins.
-  grid_dependency_wait();
-  const RowTile w = row_tile(p, b, tile, bk);
-  if (r >= w.rows) return;
-  const int used = splits_used(p, w.nblk);
-  if (used == 1) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t all = p.T * p.heads;
-  const int64_t row = (w.t0 + (w.r0 + r) / p.group) * p.heads + head * p.group + (w.r0 + r) % p.group;
-  float M = -CUDART_INF_F;
-  for (int k = lane; k < used; k += 32) M = fmaxf(M, p.part_ml[k * all + row].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float ref = M == -CUDART_INF_F ? 0.0f : M;
-  float l = 0.0f;
-  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  const bool on = 4 * lane < cv.dp;
-#pragma unroll 4
-  for (int k = warp; k < used; k += kWarps) {
-    const float2 ml = p.part_ml[k * all + row];
-    const float4 o = on ? *reinterpret_cast<const float4*>(p.part_o + (k * all + row) * cv.dp + 4 * lane) : x;
-    const float f = ex2(ml.x - ref);
-    l = __fmaf_rn(f, ml.y, l);
-    x.x = __fmaf_rn(f, o.x, x.x);
-    x.y = __fmaf_rn(f, o.y, x.y);
-    x.z = __fmaf_rn(f, o.z, x.z);
-    x.w = __fmaf_rn(f, o.w, x.w);
-  }
-  *reinterpret_cast<float4*>(&s_x[warp][4 * lane]) = x;
-  if (lane == 0) s_l[warp] = l;
-  __syncthreads();
-  const float lt = s_l[0] + s_l[1] + s_l[2] + s_l[3];
-  const int c = threadIdx.x;
-  if (c < cv.d) {
-    const float sum = s_x[0][c] + s_x[1][c] + s_x[2][c] + s_x[3][c];
-    store_out(p.o, row * cv.d + c, lt > 0.0f ? sum / lt : 0.0f, p.o_dt);
-  }
-  if (c == 0 && p.lse != nullptr) p.lse[row] = lt > 0.0f ? (M + log2f(lt)) * CUDART_LN2_F : -CUDART_INF_F;
 }
 
 template <int CPG, int NR>
@@ -804,17 +758,16 @@ cudaError_t launch_decode(const PagedAttnParams& p, int dt, cudaStream_t s) {
     cfg.numAttrs = 2;
   }
   e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<CPG, NR>, p, dt == BA_F16 ? 1 : 0, unit, map);
-  if (e != cudaSuccess || p.ctas == 0) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(p.ctas * p.row_tile));
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, line_join_kernel, p, kBlk);
+  return e != cudaSuccess || p.ctas == 0 ? e : launch_line_join(p, kBlk, s);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_join(const PagedAttnParams& p, int bk, cudaStream_t s) {
+cudaError_t launch_line_join(const PagedAttnParams& p, int bk, cudaStream_t s) {
+  // Few rows come in many parts, many rows in a few.
+  const int rows = p.row_tile > 16 ? 8 : 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.B) * p.row_tiles * p.cache.heads * p.row_tile));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.ctas * (p.row_tile / rows)));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -822,7 +775,7 @@ cudaError_t launch_paged_join(const PagedAttnParams& p, int bk, cudaStream_t s) 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel, p, bk);
+  return cudaLaunchKernelEx(&cfg, line_join_kernel, p, bk, rows);
 }
 
 cudaError_t launch_paged_decode(const PagedAttnParams& p, int dt, cudaStream_t s) {

@@ -73,12 +73,10 @@ struct PagedAttnParams {
   void* o;
   int o_dt;
   float* lse;
-  int nsplit;       // parts of the key axis (most)
-  int split_blocks; // key blocks of a part (about)
   int row_tile;    // rows (token, head of the group) of a CTA's tile
   int row_tiles;   // tiles of a sequence and KV head (most)
-  float* part_o;   // [nsplit][T * heads][dp] unnormalised sums, when nsplit > 1
-  float2* part_ml; // [nsplit][T * heads] (maximum in log2, sum)
+  float* part_o;     // [ctas][2][row_tile][dp] unnormalised sums of cut (tile, head)s, by slot
+  float2* part_ml;   // [ctas][2][row_tile] (maximum in log2, sum)
   int ctas;          // CTAs that share the line of units; 0: a cluster of CTAs per (tile, head)
   int cluster;       // its size
   JoinNote* notes;   // [ctas]
@@ -203,11 +201,6 @@ __device__ __forceinline__ Stretch find_stretch(const PagedAttnParams& p, int bk
   return st;
 }
 
-// Parts of the key axis that a tile of nblk blocks uses.
-__device__ __forceinline__ int splits_used(const PagedAttnParams& p, int nblk) {
-  return max(1, min(p.nsplit, static_cast<int>(ceil_div(nblk, p.split_blocks))));
-}
-
 // Page of the 16 tokens from j on (a multiple of 16) and their offset in it; page -1 where there is
 // none: behind the sequence, or outside the cache.
 struct PageAt {
@@ -223,17 +216,6 @@ __device__ __forceinline__ PageAt page_at(const PagedAttnParams& p, const int32_
     if (at.page < 0 || at.page >= p.cache.num_pages) at.page = -1;
   }
   return at;
-}
-
-// CTA index -> sequence, row tile, KV head and one of n parts.
-__device__ __forceinline__ void cta_of(const PagedAttnParams& p, unsigned idx, int n, int& b, int& tile, int& head,
-                                       int& part) {
-  part = idx % n;
-  idx /= n;
-  const int i = p.by_kv_heads(idx);
-  head = idx - i * p.cache.heads;
-  b = p.by_tiles(i);
-  tile = i - b * p.row_tiles;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
@@ -266,9 +248,9 @@ cudaError_t launch_paged_decode(const PagedAttnParams& p, int dt, cudaStream_t s
 cudaError_t launch_paged_chunk(const PagedAttnParams& p, int dt, cudaStream_t s);
 // Sets p's `ctas` and `cluster` for a device of `sms` SMs.
 void paged_decode_plan(PagedAttnParams* p, int sms);
-int paged_chunk_split_blocks(const PagedAttnParams& p, int sms, int* max_blocks);
-// Second kernel of a split launch: joins the parts of the row tiles (key blocks of bk tokens).
-cudaError_t launch_paged_join(const PagedAttnParams& p, int bk, cudaStream_t s);
+void paged_chunk_plan(PagedAttnParams* p, int sms);
+// The kernel behind both that joins cut (tile, head)s (key blocks of bk tokens).
+cudaError_t launch_line_join(const PagedAttnParams& p, int bk, cudaStream_t s);
 
 cudaError_t launch_cache_write(const CacheWriteParams& p, int dt, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheReadParams& p, int dt, cudaStream_t s);
