@@ -7,19 +7,22 @@
 //   O += P V   fp16: P = 2^(s - M), V = code 2^e, both numbers of the cache exact in their type
 // One CTA per SM (it owns all tensor memory) walks its stretch of the line of all key blocks, so that
 // every SM has the same number of them whatever the lengths and the mask are:
-//   * The cache holds K in bits and V in bytes; four expanding warps make the 16-bit operands in shared
-//     memory, 32 keys of a block each. A warp copies its rows with cp.async into a stage of its own, one
-//     key per lane, reads them into registers, starts the next block's copy into the same stage, and
-//     writes the operands: two instructions per pair of K channels (the pair is (c, c + 16), so that
-//     one shift and one mask place both signs; Q has the same order, and a dot product does not mind),
-//     seven per four V channels. K and V operands are double-buffered.
-//   * Two warpgroups of softmax, one per tile, one thread per row. The running maximum M moves, and O is
-//     rescaled in tensor memory, only when a score passes it by more than 2^8, which hardly ever
-//     happens after the first blocks; the weights stay far inside fp16 and the sums are fp32.
+//   * The cache holds K in bits and V in bytes. One warp brings a block's rows by TMA (V through a
+//     swizzled tensor map); four expanding warps, one key per lane, read them into registers, which
+//     frees the stage for the next block, and write the 16-bit operands: two instructions per pair of K
+//     channels (the pair is (c, c + 16), so that one shift and one mask place both signs; Q has the
+//     same order, and a dot product does not mind), seven per four V channels. K and V operands are
+//     double-buffered.
+//   * Two warpgroups of softmax, one per tile, one thread per row. Most blocks take one pass, without a
+//     maximum: the weights 2^(s - M) are made with the M of the blocks before, and their sum, which is
+//     needed anyway, shows whether any of them grew too large for fp16 (weights are positive: a sum up
+//     to 2^15 has none above). Only then, in a row's first block, and where the mask cuts a block, the
+//     scores are read twice, M moves to the maximum if that is 2^8 above it, and O is rescaled in
+//     tensor memory.
 //   * A block's scores come in two halves of 64 keys, so that a softmax warpgroup never waits for its
 //     own MMAs: one thread per tile issues the first half of the next block as soon as this block's
-//     first half has been read; its weights are made, and kept in registers, while P V and the second
-//     half of the scores run, which P's place (the second half of S) keeps apart.
+//     first half is done; its weights are made, and kept in registers, while P V and the second half of
+//     the scores run, which P's place (the second half of S) keeps apart.
 //   * At the end of a (tile, head) a softmax warpgroup writes the next one's Q before it reads O, so that
 //     the next scores are made meanwhile.
 // A block of 256 x 128 scores costs 2048 cycles of exponentials (16 per cycle and SM) and as many
@@ -34,6 +37,7 @@
 #include "kernels.h"
 #include "paged.cuh"
 #include "tc_ptx.cuh"
+#include "tensormap.h"
 
 namespace binattn {
 
@@ -48,39 +52,39 @@ constexpr int kTile = 128;     // rows per tile: M
 constexpr int kCost = 2;       // blocks that a CTA could do while it starts and ends a (tile, head)
 constexpr int kMinUnits = 4;   // units (blocks, and kCost) a CTA takes at least
 constexpr int kThreads = 512;  // service, expanding and two softmax warpgroups
-constexpr float kSlack = 8.0f;
+constexpr float kSlack = 8.0f;        // log2 by which a block's maximum may pass M
+constexpr float kMostSum = 32768.0f;  // sum of weights up to which fp16 holds each of them
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 
 template <int CH>  // channels of the operands: 64 or 128 (>= d)
 struct Cfg {
   static constexpr int kOp = kBlk * CH * 2;  // bytes of an operand tile of 128 rows
-  static constexpr int kRow = CH;            // bytes of a V row in a stage
-  static constexpr int offBits = 32 * kRow;
-  static constexpr int offMu = offBits + 32 * 16;
-  static constexpr int offExp = offMu + 32 * 2;
-  static constexpr int kStage = offExp + 32;  // a warp's 32 keys
+  static constexpr int kRow = CH;            // bytes of a V row in the stage
   static constexpr int offQ = 0;
   static constexpr int offK = offQ + 2 * kOp;
   static constexpr int offV = offK + 2 * kOp;
-  static constexpr int offRaw = offV + 2 * kOp;
-  static constexpr int offBar = offRaw + 4 * kStage;
-  static constexpr int kNumBars = 26;
-  static constexpr int offMisc = offBar + kNumBars * 8;  // tensor memory base, abort flag, page masks [4][4]
+  static constexpr int offRaw = offV + 2 * kOp;  // the cache rows of a block: codes, sign rows, mu, exponents
+  static constexpr int offBits = offRaw + kBlk * kRow;
+  static constexpr int offMu = offBits + kBlk * 16;
+  static constexpr int offExp = offMu + kBlk * 2;
+  static constexpr int offBar = offExp + kBlk;
+  static constexpr int kToken = kRow + 16 + 2 + 1;  // bytes that a token brings
+  static constexpr int kNumBars = 24;
+  static constexpr int offMisc = offBar + kNumBars * 8;  // tensor memory base, abort flag, page masks [4]
   static constexpr int offScratch = offMisc + 8 + 16;
   static constexpr int kBytes = offScratch + (kThreads / 32 + 2) * 8;
   // Tensor memory: S of tile q (P over its second half), then O.
   static __host__ __device__ constexpr uint32_t tS(int q) { return q * 128; }
   static __host__ __device__ constexpr uint32_t tO(int q) { return 256 + q * CH; }
-  // 16-byte piece c of key j's V row in a stage, moved so that eight neighbouring keys' loads of
-  // one piece touch all banks.
+  // Byte offset of the 16-byte piece c of key j's V row: the swizzle of 128- or 64-byte rows.
   static __device__ __forceinline__ int piece(int j, int c) {
     return kRow == 128 ? (j * 8 + (c ^ (j & 7))) * 16 : (j * 4 + (c ^ ((j >> 1) & 3))) * 16;
   }
 };
 
-// Barriers. K and V operands: per stage. The others: per tile; S and P by halves of the keys.
-constexpr int bKfull = 0, bKempty = 2, bVfull = 4, bVempty = 6, bQfull = 8, bS = 10, bRead = 14, bP = 16, bPV = 20,
-              bDrain = 22;
+// Barriers. K and V operands: per stage. The others: per tile; S by halves of the keys.
+constexpr int bKfull = 0, bKempty = 2, bVfull = 4, bVempty = 6, bQfull = 8, bS = 10, bRead = 14, bP = 16, bPV = 18,
+              bDrain = 20, bRawFull = 22, bRawEmpty = 23;
 
 // The (tile, head)s of a CTA one after the other, as every role walks them.
 struct Walk {
@@ -208,13 +212,13 @@ __device__ __forceinline__ float read_row(const T* src, int d, bool wide, uint32
 }
 
 template <int CH>
-__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParams p, int q_f16, int q_wide) {
+__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParams p, int q_f16, int q_wide, int unit, const __grid_constant__ CUtensorMap v_map) {
   using C = Cfg<CH>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::offBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::offMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::offMisc + 4);
-  volatile uint8_t* page_ok = smem + C::offMisc + 8;  // [block % 4][warp]: which 16-key halves have a page
+  volatile uint32_t* page_ok = reinterpret_cast<volatile uint32_t*>(smem + C::offMisc + 8);  // [block % 4]: which 16 keys have a page
   const CacheView& cv = p.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem);
@@ -230,11 +234,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
       mbar_init(&bars[bRead + i], 4);
       mbar_init(&bars[bPV + i], 1);
       mbar_init(&bars[bDrain + i], 1);
-      for (int h = 0; h < 2; ++h) {
-        mbar_init(&bars[bS + 2 * i + h], 1);
-        mbar_init(&bars[bP + 2 * i + h], 4);
-      }
+      mbar_init(&bars[bP + i], 4);
+      for (int h = 0; h < 2; ++h) mbar_init(&bars[bS + 2 * i + h], 1);
     }
+    mbar_init(&bars[bRawFull], 1);
+    mbar_init(&bars[bRawEmpty], 4);
     *abort_flag = 0;
     mbar_fence_init();
     fence_proxy_async_smem();
@@ -258,20 +262,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
       const uint32_t id_qk = (1u << 4) | (1u << 7) | (1u << 10) | ((kBlk / 2 >> 3) << 17) | ((kTile >> 4) << 24);
       const uint32_t id_pv = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(cv.dp >> 3) << 17) | ((kTile >> 4) << 24);
       const int qk_steps = 2 * ((cv.d + 31) / 32);
-      const uint32_t qa = base + C::offQ + q * C::kOp, s_t = tmem + C::tS(q), o_t = tmem + C::tO(q);
+      const uint32_t s_t = tmem + C::tS(q), o_t = tmem + C::tO(q);
+      // Descriptors: the address part (in units of 16 bytes) of the first step, and what is fixed.
+      const uint64_t k_desc = smem_desc(0, 2048, 128), v_desc = smem_desc(0, 128, 2048);
+      const uint32_t q_at = (base + C::offQ + q * C::kOp) >> 4, k_at = (base + C::offK) >> 4, v_at = (base + C::offV) >> 4;
       // Scores of the keys 64 h .. 64 h + 63 of the block in stage st.
       auto qk = [&](int st, int h) {
-        const uint32_t ka = base + C::offK + st * C::kOp + h * 1024;
-        for (int i = 0; i < qk_steps; ++i)
-          mma_f16_ss(s_t + 64 * h, smem_desc(qa + i * 4096, 2048, 128), smem_desc(ka + i * 4096, 2048, 128), id_qk,
-                     i > 0 ? 1u : 0u);
+        const uint32_t ka = k_at + st * (C::kOp / 16) + h * 64;
+#pragma unroll
+        for (int i = 0; i < CH / 16; ++i)
+          if (i < qk_steps)
+            mma_f16_ss(s_t + 64 * h, k_desc | (q_at + i * 256), k_desc | (ka + i * 256), id_qk, i > 0 ? 1u : 0u);
         tc_commit(&bars[bS + 2 * q + h]);
       };
-      auto pv = [&](int st, int h, bool first) {
-        const uint32_t va = base + C::offV + st * C::kOp + h * 1024;
+      auto pv = [&](int st, uint32_t more) {
+        const uint32_t va = v_at + st * (C::kOp / 16);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          mma_f16_ts(o_t, s_t + 64 + 32 * h + 8 * i, smem_desc(va + 256 * i, 128, 2048), id_pv, first && i == 0 ? 0u : 1u);
+        for (int i = 0; i < kBlk / 16; ++i)
+          mma_f16_ts(o_t, s_t + 64 + 8 * i, v_desc | (va + 16 * i), id_pv, i > 0 ? 1u : more);
       };
       int g = 0, c = 0, seg = 0;  // blocks of the CTA, blocks and (tile, head)s of this tile so far
       bool ok = true;
@@ -299,12 +307,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
             tc_fence_after();
             qk((g + 1) & 1, 0);
           }
-          if (!wait(bP + 2 * q, c) || !wait(bVfull + (g & 1), g >> 1)) break;
+          if (!wait(bP + q, c) || !wait(bVfull + (g & 1), g >> 1)) break;
           tc_fence_after();
-          pv(g & 1, 0, n == 0);
-          if (!wait(bP + 2 * q + 1, c)) break;
-          tc_fence_after();
-          pv(g & 1, 1, false);
+          pv(g & 1, n > 0 ? 1u : 0u);
           tc_commit(&bars[bPV + q]);
           tc_commit(&bars[bVempty + (g & 1)]);
           if (more) {
@@ -318,68 +323,76 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
       wait_bar<true>(&bars[bDrain + q], 0, abort_flag, false);
     }
     __syncwarp();
+    if (warp == 2) {
+      // ---------------------------------------------------------- a block's cache rows
+      // A block comes as `per` pieces of `unit` tokens, each within a page. Lane l keeps the page and
+      // the offset in it of the piece l % 8 of the block l / 8 after the last look-up. Lane 4 i + k
+      // brings, of piece i, the V rows (k = 0), the sign rows, mu or the exponents.
+      const int per = kBlk / unit, piece = lane >> 2, kind = lane & 3;
+      const int xoff = kind == 1 ? cv.off_bits() : (kind == 2 ? cv.off_mu() : cv.off_exp());
+      const int xsize = kind == 1 ? 16 : (kind == 2 ? 2 : 1);
+      const uint32_t extra = base + (kind == 1 ? C::offBits : (kind == 2 ? C::offMu : C::offExp)) + unit * piece * xsize;
+      const uint32_t bar = smem_u32(&bars[bRawFull]);
+      int g = 0;
+      bool ok = true;
+      while (ok && k.next(p)) {
+        const int32_t* table = p.table + k.b * p.table_stride;
+        PageAt at{-1, 0};
+        for (int n = 0; n < k.n_blk; ++n, ++g) {
+          if ((n & 3) == 0) {
+            at.page = -1;
+            const int m = n + (lane >> 3);
+            if (m < k.n_blk && (lane & 7) < per)
+              at = page_at(p, table, k.w.kv, k.w.block_at(k.v0 + m) * kBlk + (lane & 7) * unit);
+          }
+          const int page = __shfl_sync(0xffffffffu, at.page, 8 * (n & 3) + piece);
+          const int off = __shfl_sync(0xffffffffu, at.off, 8 * (n & 3) + piece);
+          // Bits 0, 4, .. 28 of the vote: the pieces with a page; `have`: the 16-key parts with one.
+          const uint32_t vote = __ballot_sync(0xffffffffu, page >= 0 && piece < per) & 0x11111111u;
+          const uint32_t have = __ballot_sync(0xffffffffu, lane < 8 && (vote >> (4 * (lane * kPageUnit / unit))) & 1u);
+          if (g > 0 && !(ok = wait_warp<true>(&bars[bRawEmpty], (g - 1) & 1, abort_flag))) break;
+          if (lane == 0) {
+            page_ok[g & 3] = have;
+            mbar_arrive_expect_tx(&bars[bRawFull], __popc(vote) * unit * C::kToken);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (piece < per) {
+            if (page < 0) {
+              // No page: the rows are not seen, but what their scores are made of stays finite.
+              if (kind > 0)
+                for (int i = 0; i < unit / 16 * xsize; ++i) sts128(extra + 16 * i, 0u, 0u, 0u, 0u);
+            } else if (kind == 0) {
+              tma_load_3d(base + C::offRaw + unit * piece * C::kRow, &v_map, bar, 0, off, page * cv.heads + k.head);
+            } else {
+              bulk_load(extra, cv.block(page, k.head) + xoff + off * xsize, unit * xsize, bar);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      // Nothing on its way when the CTA ends.
+      if (g > 0) wait_bar<true>(&bars[bRawFull], (g - 1) & 1, abort_flag, false);
+    }
   } else if (warp < 8) {
     // ------------------------------------------------------------ expanding K and V
     setmaxnreg_dec<88>();
-    const int ew = warp - 4;
-    const uint32_t raw = base + C::offRaw + ew * C::kStage;
-    const int row = ew * 32 + lane;  // key of the block
+    const int row = (warp - 4) * 32 + lane;  // key of the block
     int g = 0;
     bool ok = true;
     while (ok && k.next(p)) {
-      const int n_blk = k.n_blk, head = k.head;
-      const int32_t* table = p.table + k.b * p.table_stride;
-      PageAt at{-1, 0};
-      uint32_t have = 0;
-      auto issue = [&](int n) {
-        if (n >= n_blk) return;
-        if ((n & 15) == 0) {
-          at.page = -1;
-          if (n + (lane >> 1) < n_blk)
-            at = page_at(p, table, k.w.kv, k.w.block_at(k.v0 + n + (lane >> 1)) * kBlk + ew * 32 + (lane & 1) * kPageUnit);
-        }
-        have = 0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int page = __shfl_sync(0xffffffffu, at.page, 2 * (n & 15) + h);
-          const int off = __shfl_sync(0xffffffffu, at.off, 2 * (n & 15) + h);
-          const bool is = page >= 0;
-          have |= (is ? 1u : 0u) << h;
-          const uint8_t* blk = is ? cv.block(page, head) : cv.data;
-          constexpr int PPR = C::kRow / 16;
-#pragma unroll
-          for (int i = 0; i < kPageUnit * PPR / 32; ++i) {
-            const int idx = lane + 32 * i, j = idx / PPR, c = idx % PPR;
-            if (c * 16 < cv.dp)
-              cp_async16(raw + C::piece(kPageUnit * h + j, c), is ? blk + (off + j) * cv.dp + c * 16 : blk, is);
-          }
-          if (lane < 19) {
-            const uint8_t* src = lane < 16 ? blk + cv.off_bits() + (off + lane) * 16
-                                           : (lane < 18 ? blk + cv.off_mu() + off * 2 + (lane - 16) * 16
-                                                        : blk + cv.off_exp() + off);
-            const uint32_t to = lane < 16 ? C::offBits + (kPageUnit * h + lane) * 16
-                                          : (lane < 18 ? C::offMu + kPageUnit * h * 2 + (lane - 16) * 16
-                                                       : C::offExp + kPageUnit * h);
-            cp_async16(raw + to, is ? src : blk, is);
-          }
-        }
-        cp_async_commit();
-      };
-      issue(0);
-      for (int n = 0; n < n_blk; ++n, ++g) {
-        cp_async_wait<0>();
-        __syncwarp();
-        const uint4 bits = lds128(raw + C::offBits + lane * 16);
-        const uint32_t mu = lds16(raw + C::offMu + lane * 2);
-        const int e8 = static_cast<int8_t>(lds16(raw + C::offExp + (lane & ~1)) >> (8 * (lane & 1)));
+      for (int n = 0; n < k.n_blk; ++n, ++g) {
+        const int st = g & 1;
+        if (!(ok = wait_warp<true>(&bars[bRawFull], g & 1, abort_flag))) break;
+        const uint4 bits = lds128(base + C::offBits + row * 16);
+        const uint32_t mu = lds16(base + C::offMu + row * 2);
+        const int e8 = static_cast<int8_t>(lds16(base + C::offExp + (row & ~1)) >> (8 * (row & 1)));
         uint4 code[CH / 16];
 #pragma unroll
         for (int c = 0; c < CH / 16; ++c)
-          if (c * 16 < cv.dp) code[c] = lds128(raw + C::piece(lane, c));
-        if (lane == 0) page_ok[(g & 3) * 4 + ew] = static_cast<uint8_t>(have);
+          if (c * 16 < cv.dp) code[c] = lds128(base + C::offRaw + C::piece(row, c));
         __syncwarp();
-        issue(n + 1);
-        const int st = g & 1;
+        if (lane == 0) mbar_arrive(&bars[bRawEmpty]);
         if (g >= 2 && !(ok = wait_warp<true>(&bars[bKempty + st], ((g >> 1) - 1) & 1, abort_flag))) break;
         const uint32_t kd = base + C::offK + st * C::kOp + row * 16;
         const uint32_t word[4] = {bits.x, bits.y, bits.z, bits.w};
@@ -406,7 +419,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[bVfull + st]);
       }
-      cp_async_wait<0>();
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -480,93 +492,104 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
         }
         return f;
       };
+      auto arrive = [&](int bar) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[bar]);
+      };
+      auto read = [&](int at, uint32_t (&s)[32]) { tmem_ld32p(aS + at, s); };
+      auto arrived = [&](uint32_t (&s)[32]) {
+        tmem_ld_wait();
+        reg_fence32(s);
+      };
+      // Weights of 32 keys as 16 fp16 pairs; their sums are added to `sum`.
+      auto weigh = [&](const uint32_t (&s)[32], uint32_t* to, float ref, float2 (&sum)[2]) {
+        const float2 c2 = make_float2(cq, cq), m2 = make_float2(-ref, -ref);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, m2);
+          const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+          sum[i & 1] = __fadd2_rn(sum[i & 1], e);
+          const __half2 y = __floats2half2_rn(e.x, e.y);
+          to[i] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+      };
       for (int n = 0; n < n_blk && mine && ok; ++n, ++g, ++c) {
         const int j0 = w.block_at(v0 + n) * kBlk;
-        uint32_t have = 0, pa[32];
-        bool whole = false;
-#pragma unroll 1
+        uint32_t pw[2][32];
+        bool one_pass = false;
+        uint32_t have = 0;
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t s[64];
           if (!(ok = wait_warp<false>(&bars[bS + 2 * q + h], c & 1, abort_flag))) break;
           tc_fence_after();
-          tmem_ld32p(aS + 64 * h, s);
-          tmem_ld32p(aS + 64 * h + 32, s + 32);
           if (h == 0) {
-            have = *reinterpret_cast<volatile uint32_t*>(smem + C::offMisc + 8 + (g & 3) * 4);
-            whole = have == 0x03030303u && j0 + kBlk - 1 <= all_last && j0 >= all_lo;
+            have = page_ok[g & 3];
+            one_pass = have == 0xffu && j0 + kBlk - 1 <= all_last && j0 >= all_lo &&
+                       !__any_sync(0xffffffffu, live && M == -CUDART_INF_F);
           }
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) reg_fence8(s + 8 * i);
-          if (h == 0) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[bRead + q]);
+          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+          bool done = false;
+          if (one_pass) {
+            uint32_t x[32], y[32];
+            read(64 * h, x);
+            arrived(x);
+            read(64 * h + 32, y);
+            weigh(x, pw[h], M, sum);
+            arrived(y);
+            weigh(y, pw[h] + 16, M, sum);
+            done = __all_sync(0xffffffffu, !live || (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y) <= kMostSum);
           }
-          if (!whole) {
-            __syncwarp();  // keeps this a branch
+          if (!done) {
+            // The keys that this row sees, by 32.
+            uint32_t see[2], x[32];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {  // which of 32 keys this row sees
+            for (int k = 0; k < 2; ++k) {
               const int j = j0 + 64 * h + 32 * k;
-              const uint32_t pages = have >> (8 * (2 * h + k));
-              const uint32_t see = low_bits(last - j + 1) & (~low_bits(wlo - j) | low_bits(p.sinks - j)) &
-                                   ((pages & 1u) * 0xffffu | (pages >> 1 & 1u) * 0xffff0000u);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((see >> i) & 1u)) s[32 * k + i] = 0xff800000u;  // -inf
+              const uint32_t pages = have >> (4 * h + 2 * k);
+              see[k] = low_bits(last - j + 1) & (~low_bits(wlo - j) | low_bits(p.sinks - j)) &
+                       ((pages & 1u) * 0xffffu | (pages >> 1 & 1u) * 0xffff0000u);
             }
-          }
-          float mx[4];
+            float top = -CUDART_INF_F;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = fmax3(__uint_as_float(s[i]), __uint_as_float(s[i + 4]), __uint_as_float(s[i + 8]));
+            for (int k = 0; k < 2; ++k) {
+              read(64 * h + 32 * k, x);
+              arrived(x);
 #pragma unroll
-          for (int j = 12; j < 60; j += 8)
+              for (int i = 0; i < 32; ++i) top = fmaxf(top, (see[k] >> i) & 1u ? __uint_as_float(x[i]) : -CUDART_INF_F);
+            }
+            top *= cq;
+            if (__any_sync(0xffffffffu, top > M + kSlack)) {
+              const float f = move_to(top, n);
+              if (!ok) break;
+              if (h == 1) {  // the first half's weights, already fp16, are rounded once more
+                const __half2 f2 = __float2half2_rn(f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mx[i] = fmax3(mx[i], __uint_as_float(s[j + i]), __uint_as_float(s[j + 4 + i]));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], __uint_as_float(s[60 + i]));
-          const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * cq;
-          if (__any_sync(0xffffffffu, top > M + kSlack)) {
-            const float f = move_to(top, n);
-            if (!ok) break;
-            if (h == 1) {  // the first half's weights, already fp16, are rounded once more
-              const __half2 f2 = __float2half2_rn(f);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&pa[i]), f2);
-                pa[i] = *reinterpret_cast<const uint32_t*>(&y);
+                for (int i = 0; i < 32; ++i) {
+                  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&pw[0][i]), f2);
+                  pw[0][i] = *reinterpret_cast<const uint32_t*>(&y);
+                }
               }
             }
-          }
-          if (h == 1) {  // the second half of S has been read: P may go there
-            tmem_st32p(aS + 64, pa);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[bP + 2 * q]);
-          }
-          const float ref = M == -CUDART_INF_F ? 0.0f : M;
-          const float2 c2 = make_float2(cq, cq), m2 = make_float2(-ref, -ref);
-          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            sum[0] = sum[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, m2);
-            const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-            sum[i & 1] = __fadd2_rn(sum[i & 1], e);
-            const __half2 y = __floats2half2_rn(e.x, e.y);
-            pa[i] = *reinterpret_cast<const uint32_t*>(&y);
+            for (int k = 0; k < 2; ++k) {
+              read(64 * h + 32 * k, x);
+              arrived(x);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((see[k] >> i) & 1u)) x[i] = 0xff800000u;  // -inf
+              weigh(x, pw[h] + 16 * k, M == -CUDART_INF_F ? 0.0f : M, sum);
+            }
           }
-          sum[0] = __fadd2_rn(sum[0], sum[1]);
-          l += sum[0].x + sum[0].y;
-          if (h == 1) {
-            tmem_st32p(aS + 96, pa);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[bP + 2 * q + 1]);
-          }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          if (h == 0) arrive(bRead + q);
         }
         if (!ok) break;
+        tmem_st32p(aS + 64, pw[0]);
+        tmem_st32p(aS + 96, pw[1]);
+        tmem_st_wait();
+        arrive(bP + q);
       }
       if (!ok) break;
       // The next (tile, head)'s scores can be made while this one's rows are written.
@@ -648,7 +671,10 @@ cudaError_t launch_chunk(const PagedAttnParams& p, int dt, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const bool wide = p.cache.d % 8 == 0 && reinterpret_cast<uintptr_t>(p.q) % 16 == 0 &&
                     (p.q_stride_t | p.q_stride_h) % 8 == 0;
-  paged_chunk_kernel<CH><<<p.ctas, kThreads, smem, s>>>(p, dt == BA_F16 ? 1 : 0, wide ? 1 : 0);
+  const int unit = v_unit(p.cache, kBlk);
+  CUtensorMap map;
+  if (!v_rows_map(p.cache, CH, unit, &map)) return cudaErrorInvalidValue;
+  paged_chunk_kernel<CH><<<p.ctas, kThreads, smem, s>>>(p, dt == BA_F16 ? 1 : 0, wide ? 1 : 0, unit, map);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_line_join(p, kBlk, s);
 }

@@ -722,23 +722,10 @@ cudaError_t launch_decode(const PagedAttnParams& p, int dt, cudaStream_t s) {
   constexpr int smem = Ring<CPG>::total(8 * NR);
   cudaError_t e = allow_smem<paged_decode_kernel<CPG, NR>>(smem);
   if (e != cudaSuccess) return e;
-  // The V rows of all blocks, as (byte, token, block); a copy brings `unit` rows of a page, padded to
-  // CPG * 8 bytes.
-  EncodeTiledFn enc = encode_fn();
-  if (enc == nullptr) return cudaErrorNotSupported;
   const CacheView& cv = p.cache;
-  const int unit = cv.page_size % 64 == 0 ? 64 : (cv.page_size % 32 == 0 ? 32 : 16);
-  CUtensorMap map{};
-  if (cv.num_pages > 0) {
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cv.dp), static_cast<cuuint64_t>(cv.page_size),
-                                static_cast<cuuint64_t>(cv.num_pages) * cv.heads};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cv.dp), static_cast<cuuint64_t>(cv.block_bytes)};
-    const cuuint32_t box[3] = {CPG * 8, static_cast<cuuint32_t>(unit), 1}, step[3] = {1, 1, 1};
-    if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, cv.data, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CPG == 16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
-  }
+  const int unit = v_unit(cv, kBlk);
+  CUtensorMap map;
+  if (!v_rows_map(cv, CPG * 8, unit, &map)) return cudaErrorInvalidValue;
   const int64_t tiles = static_cast<int64_t>(p.B) * p.row_tiles * cv.heads;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
