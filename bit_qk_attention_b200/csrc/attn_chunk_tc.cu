@@ -182,37 +182,8 @@ __device__ __forceinline__ void expand_codes(uint32_t dst, uint32_t a, uint32_t 
   sts128(dst, x[0], x[1], x[2], x[3]);
 }
 
-// Sign words and sum of |x| of one row of q.
-template <typename T>
-__device__ __forceinline__ float read_row(const T* src, int d, bool wide, uint32_t (&word)[4]) {
-  float sum = 0.0f;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    word[k] = 0u;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int c0 = 32 * k + 8 * c;
-      float f[8];
-      if (wide) {
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (c0 < d) u = __ldg(reinterpret_cast<const uint4*>(src + c0));
-        unpack8<T>(u, f);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = c0 + i < d ? load1<T>(src + c0 + i) : 0.0f;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        word[k] |= (f[i] < 0.0f ? 1u : 0u) << (8 * c + i);
-        sum += fabsf(f[i]);
-      }
-    }
-  }
-  return sum;
-}
-
 template <int CH>
-__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParams p, int q_f16, int q_wide, int unit, const __grid_constant__ CUtensorMap v_map) {
+__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParams p, int q_f16, int unit, const __grid_constant__ CUtensorMap v_map) {
   using C = Cfg<CH>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::offBar);
@@ -428,27 +399,54 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
     const uint32_t lane_base = static_cast<uint32_t>(w4 * 32) << 16;
     const uint32_t aS = tmem + lane_base + C::tS(q), aO = tmem + lane_base + C::tO(q);
     int g = 0, c = 0;
-    // Q of the (tile, head) `to` and the factor of its scores.
+    // Q of the (tile, head) `to` and the factor of its scores. The warp takes its rows one after the
+    // other, a channel per lane and word, and each lane keeps its own row's signs and sum. (Little code
+    // is what counts here: it runs once per (tile, head), when its instructions are not in any cache.)
     auto write_q = [&](const Walk& to) {
-      float cq = 1e-30f;  // above 0 also for a row of zeros, so that -inf in masked places stays -inf
       uint32_t word[4] = {0u, 0u, 0u, 0u};
-      if (r < to.w.rows) {
-        const int i = p.by_group(to.w.r0 + r);
-        const int64_t at = (to.w.t0 + i) * p.q_stride_t + (to.head * p.group + to.w.r0 + r - i * p.group) * p.q_stride_h;
-        const float sum = q_f16 ? read_row(static_cast<const __half*>(p.q) + at, cv.d, q_wide, word)
-                                : read_row(static_cast<const __nv_bfloat16*>(p.q) + at, cv.d, q_wide, word);
-        cq = fmaxf(p.scale_log2 * (sum / static_cast<float>(cv.d)), cq);
+      float total = 0.0f;
+      const int rows = min(32, to.w.rows - (r - lane));
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows; r0 += 4) {
+        uint16_t raw[4][CH / 32];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int row = to.w.r0 + min(r - lane + r0 + u, to.w.rows - 1), i = p.by_group(row);
+          const uint16_t* src = static_cast<const uint16_t*>(p.q) + (to.w.t0 + i) * p.q_stride_t +
+                                (to.head * p.group + row - i * p.group) * p.q_stride_h;
+#pragma unroll
+          for (int x = 0; x < CH / 32; ++x) raw[u][x] = 32 * x + lane < cv.d ? __ldg(src + 32 * x + lane) : uint16_t{0};
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float sum = 0.0f;
+          uint32_t neg[CH / 32];
+#pragma unroll
+          for (int x = 0; x < CH / 32; ++x) {
+            const float f = widen(raw[u][x], q_f16);
+            neg[x] = __ballot_sync(0xffffffffu, f < 0.0f);
+            sum += fabsf(f);
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (lane == r0 + u) {
+            total = sum;
+#pragma unroll
+            for (int x = 0; x < CH / 32; ++x) word[x] = neg[x];
+          }
+        }
       }
       const uint32_t qd = base + C::offQ + q * C::kOp + (w4 * 32 + lane) * 16;
 #pragma unroll
       for (int i = 0; i < CH / 32; ++i) {
         const int n = cv.d - 32 * i;
-        if (n > 0) expand_signs(qd + i * 8192, word[i], 0x3f803f80u, n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+        if (n > 0) expand_signs(qd + i * 8192, word[i], 0x3f803f80u, low_bits(n));
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[bQfull + q]);
-      return cq;
+      // Above 0 also for a row of zeros, so that -inf in masked places stays -inf.
+      return fmaxf(p.scale_log2 * (total / static_cast<float>(cv.d)), 1e-30f);
     };
     bool ok = true, more = k.next(p);
     float cq_next = 1e-30f;
@@ -516,21 +514,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
       };
       for (int n = 0; n < n_blk && mine && ok; ++n, ++g, ++c) {
         const int j0 = w.block_at(v0 + n) * kBlk;
+        if (!(ok = wait_warp<false>(&bars[bS + 2 * q], c & 1, abort_flag))) break;
+        tc_fence_after();
+        const uint32_t have = page_ok[g & 3];
+        // Quarters (32 keys) from here on are read twice.
+        int again = have == 0xffu && j0 + kBlk - 1 <= all_last && j0 >= all_lo &&
+                    !__any_sync(0xffffffffu, live && M == -CUDART_INF_F) ? 4 : 0;
         uint32_t pw[2][32];
-        bool one_pass = false;
-        uint32_t have = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (!(ok = wait_warp<false>(&bars[bS + 2 * q + h], c & 1, abort_flag))) break;
-          tc_fence_after();
-          if (h == 0) {
-            have = page_ok[g & 3];
-            one_pass = have == 0xffu && j0 + kBlk - 1 <= all_last && j0 >= all_lo &&
-                       !__any_sync(0xffffffffu, live && M == -CUDART_INF_F);
+          if (h == 1) {
+            if (!(ok = wait_warp<false>(&bars[bS + 2 * q + 1], c & 1, abort_flag))) break;
+            tc_fence_after();
           }
-          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-          bool done = false;
-          if (one_pass) {
+          if (again == 4) {
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
             uint32_t x[32], y[32];
             read(64 * h, x);
             arrived(x);
@@ -538,56 +536,66 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
             weigh(x, pw[h], M, sum);
             arrived(y);
             weigh(y, pw[h] + 16, M, sum);
-            done = __all_sync(0xffffffffu, !live || (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y) <= kMostSum);
-          }
-          if (!done) {
-            // The keys that this row sees, by 32.
-            uint32_t see[2], x[32];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int j = j0 + 64 * h + 32 * k;
-              const uint32_t pages = have >> (4 * h + 2 * k);
-              see[k] = low_bits(last - j + 1) & (~low_bits(wlo - j) | low_bits(p.sinks - j)) &
-                       ((pages & 1u) * 0xffffu | (pages >> 1 & 1u) * 0xffff0000u);
-            }
-            float top = -CUDART_INF_F;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              read(64 * h + 32 * k, x);
-              arrived(x);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) top = fmaxf(top, (see[k] >> i) & 1u ? __uint_as_float(x[i]) : -CUDART_INF_F);
-            }
-            top *= cq;
-            if (__any_sync(0xffffffffu, top > M + kSlack)) {
-              const float f = move_to(top, n);
-              if (!ok) break;
-              if (h == 1) {  // the first half's weights, already fp16, are rounded once more
-                const __half2 f2 = __float2half2_rn(f);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&pw[0][i]), f2);
-                  pw[0][i] = *reinterpret_cast<const uint32_t*>(&y);
-                }
-              }
-            }
-            sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              read(64 * h + 32 * k, x);
-              arrived(x);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((see[k] >> i) & 1u)) x[i] = 0xff800000u;  // -inf
-              weigh(x, pw[h] + 16 * k, M == -CUDART_INF_F ? 0.0f : M, sum);
+            const float all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            if (__all_sync(0xffffffffu, !live || all <= kMostSum)) {
+              l += all;
+              if (h == 0) arrive(bRead + q);
+            } else {
+              again = 2 * h;
             }
           }
-          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-          if (h == 0) arrive(bRead + q);
         }
         if (!ok) break;
-        tmem_st32p(aS + 64, pw[0]);
-        tmem_st32p(aS + 96, pw[1]);
+        if (again < 4) {
+          float top = -CUDART_INF_F;
+          uint32_t x[32];
+          // Which of its 32 keys the row sees.
+          auto seen = [&](int quarter) {
+            const int j = j0 + 32 * quarter;
+            const uint32_t pages = have >> (2 * quarter);
+            return low_bits(last - j + 1) & (~low_bits(wlo - j) | low_bits(p.sinks - j)) &
+                   ((pages & 1u) * 0xffffu | (pages >> 1 & 1u) * 0xffff0000u);
+          };
+#pragma unroll 1
+          for (int k = again; k < 4; ++k) {
+            read(32 * k, x);
+            const uint32_t see = seen(k);
+            arrived(x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) top = fmaxf(top, (see >> i) & 1u ? __uint_as_float(x[i]) : -CUDART_INF_F);
+          }
+          top *= cq;
+          if (__any_sync(0xffffffffu, top > M + kSlack)) {
+            const float f = move_to(top, n);
+            if (!ok) break;
+            if (again == 2) {  // the first half's weights, already fp16, are rounded once more
+              const __half2 f2 = __float2half2_rn(f);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&pw[0][i]), f2);
+                pw[0][i] = *reinterpret_cast<const uint32_t*>(&y);
+              }
+            }
+          }
+          // From the last quarter down: P of a quarter lies over scores that have been read.
+          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll 1
+          for (int k = 3; k >= again; --k) {
+            read(32 * k, x);
+            const uint32_t see = seen(k);
+            arrived(x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((see >> i) & 1u)) x[i] = 0xff800000u;  // -inf
+            uint32_t y[16];
+            weigh(x, y, M == -CUDART_INF_F ? 0.0f : M, sum);
+            tmem_st16p(aS + 64 + 16 * k, y);
+          }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          if (again == 0) arrive(bRead + q);
+        }
+        if (again > 0) tmem_st32p(aS + 64, pw[0]);
+        if (again == 4) tmem_st32p(aS + 96, pw[1]);
         tmem_st_wait();
         arrive(bP + q);
       }
@@ -669,12 +677,10 @@ cudaError_t launch_chunk(const PagedAttnParams& p, int dt, cudaStream_t s) {
   const int smem = std::max(Cfg<CH>::kBytes, 116 * 1024);
   cudaError_t e = allow_smem<paged_chunk_kernel<CH>>(smem);
   if (e != cudaSuccess) return e;
-  const bool wide = p.cache.d % 8 == 0 && reinterpret_cast<uintptr_t>(p.q) % 16 == 0 &&
-                    (p.q_stride_t | p.q_stride_h) % 8 == 0;
   const int unit = v_unit(p.cache, kBlk);
   CUtensorMap map;
   if (!v_rows_map(p.cache, CH, unit, &map)) return cudaErrorInvalidValue;
-  paged_chunk_kernel<CH><<<p.ctas, kThreads, smem, s>>>(p, dt == BA_F16 ? 1 : 0, wide ? 1 : 0, unit, map);
+  paged_chunk_kernel<CH><<<p.ctas, kThreads, smem, s>>>(p, dt == BA_F16 ? 1 : 0, unit, map);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_line_join(p, kBlk, s);
 }

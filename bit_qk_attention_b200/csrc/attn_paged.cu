@@ -171,11 +171,6 @@ __device__ __forceinline__ float lds_cluster(uint32_t a, int rank) {
   return x;
 }
 
-// A 16-bit number, widened.
-__device__ __forceinline__ float widen(uint16_t x, int f16) {
-  return f16 ? __half2float(__ushort_as_half(x)) : __uint_as_float(static_cast<uint32_t>(x) << 16);
-}
-
 template <int CPG, int NR>
 __global__ void __launch_bounds__(kThreads, 3)
     paged_decode_kernel(PagedAttnParams p, int q_f16, int unit, const __grid_constant__ CUtensorMap v_map) {
