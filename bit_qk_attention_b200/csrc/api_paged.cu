@@ -17,6 +17,7 @@ constexpr int64_t kMaxRows = int64_t{1} << 31;  // (token, head) rows of a call
 constexpr int64_t kMaxKv = int64_t{1} << 28;
 // Rows (new tokens x heads of a group) per sequence up to which the decoding kernel is taken.
 constexpr int kDecodeRows = 32;
+constexpr int kChunkRows = 256;  // row tile of the kernel for more
 constexpr int64_t kMaxCtas = (int64_t{1} << 31) - 1;
 
 bool aligned(const void* p, unsigned n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -58,12 +59,16 @@ size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 size_t line_workspace(const PagedAttnParams& p, PagedAttnParams* out) {
   const size_t n = static_cast<size_t>(p.ctas) * 2 * p.row_tile;
   const size_t ml = align_up(n * p.cache.dp * 4), notes = ml + align_up(n * 8);
+  const size_t bits = notes + align_up(static_cast<size_t>(p.ctas) * sizeof(JoinNote));
+  const size_t rows = p.row_tile == kChunkRows ? static_cast<size_t>(p.T) * p.heads : 0, mu = bits + align_up(rows * 16);
   if (out != nullptr) {
     char* base = reinterpret_cast<char*>(out->part_o);
     out->part_ml = reinterpret_cast<float2*>(base + ml);
     out->notes = reinterpret_cast<JoinNote*>(base + notes);
+    out->q_bits = reinterpret_cast<uint4*>(base + bits);
+    out->q_mu = reinterpret_cast<float*>(base + mu);
   }
-  return notes + align_up(static_cast<size_t>(p.ctas) * sizeof(JoinNote));
+  return mu + align_up(rows * 4);
 }
 
 // Everything of a call that does not depend on its tensors: sizes, the kernel's tiles and splits,
@@ -95,7 +100,7 @@ ba_status plan(const ba_kv_cache* cache, const ba_paged_seqs* s, PagedAttnParams
   p->sinks = s->sinks;
   if (p->B == 0 || p->max_q_len == 0) return BA_OK;  // nothing to launch
   const int64_t rows = static_cast<int64_t>(p->max_q_len) * p->group;
-  p->row_tile = rows <= 8 ? 8 : (rows <= kDecodeRows ? 16 : 256);
+  p->row_tile = rows <= 8 ? 8 : (rows <= kDecodeRows ? 16 : kChunkRows);
   const int64_t tiles = ceil_div(rows, p->row_tile);
   if (tiles > kMaxCtas / (static_cast<int64_t>(p->B) * p->cache.heads)) return BA_ERR_UNSUPPORTED;
   p->row_tiles = static_cast<int>(tiles);
@@ -104,7 +109,7 @@ ba_status plan(const ba_kv_cache* cache, const ba_paged_seqs* s, PagedAttnParams
   p->by_page = FastDiv::of(p->cache.page_size);
   p->by_tiles = FastDiv::of(p->row_tiles);
   if (tiles * p->B * p->cache.heads > kMaxCtas / p->row_tile) return BA_ERR_UNSUPPORTED;
-  if (p->row_tile == 256)
+  if (p->row_tile == kChunkRows)
     paged_chunk_plan(p, sm_count());
   else
     paged_decode_plan(p, sm_count());
@@ -200,7 +205,7 @@ ba_status ba_attention_paged(const void* q, int64_t q_stride_t, int64_t q_stride
   p.o_dt = o_dt;
   p.lse = lse;
   const cudaStream_t st_ = static_cast<cudaStream_t>(stream);
-  return report_cuda(p.row_tile == 256 ? launch_paged_chunk(p, dt, st_) : launch_paged_decode(p, dt, st_));
+  return report_cuda(p.row_tile == kChunkRows ? launch_paged_chunk(p, dt, st_) : launch_paged_decode(p, dt, st_));
 }
 
 }  // extern "C"

@@ -16,13 +16,12 @@
 //   * Two warpgroups of softmax, one per tile, one thread per row. Most blocks take one pass, without a
 //     maximum: the weights 2^(s - M) are made with the M of the blocks before, and their sum, which is
 //     needed anyway, shows whether any of them grew too large for fp16 (weights are positive: a sum up
-//     to 2^15 has none above). Only then, in a row's first block, and where the mask cuts a block, the
-//     scores are read twice, M moves to the maximum if that is 2^8 above it, and O is rescaled in
-//     tensor memory.
-//   * A block's scores come in two halves of 64 keys, so that a softmax warpgroup never waits for its
-//     own MMAs: one thread per tile issues the first half of the next block as soon as this block's
-//     first half is done; its weights are made, and kept in registers, while P V and the second half of
-//     the scores run, which P's place (the second half of S) keeps apart.
+//     to 2^15 has none above). Only then, and in a row's first block, the scores are read twice, M moves
+//     to the maximum if that is 2^8 above it, and O is rescaled in tensor memory.
+//   * A block's scores come in two halves of 64 keys, so that a softmax warpgroup hardly waits for its
+//     own MMAs: the first half of the next block is issued as soon as this block's first half is done;
+//     its weights are made, and kept in registers, while P V and the second half of the scores run,
+//     which P's place (the second half of S) keeps apart.
 //   * At the end of a (tile, head) a softmax warpgroup writes the next one's Q before it reads O, so that
 //     the next scores are made meanwhile.
 // A block of 256 x 128 scores costs 2048 cycles of exponentials (16 per cycle and SM) and as many
@@ -53,7 +52,8 @@ constexpr int kCost = 2;       // blocks that a CTA could do while it starts and
 constexpr int kMinUnits = 4;   // units (blocks, and kCost) a CTA takes at least
 constexpr int kThreads = 512;  // service, expanding and two softmax warpgroups
 constexpr float kSlack = 8.0f;        // log2 by which a block's maximum may pass M
-constexpr float kMostSum = 32768.0f;  // sum of weights up to which fp16 holds each of them
+constexpr float kMostLog2 = 15.0f;    // log2 of weights that fp16 surely holds
+constexpr float kMostSum = 32768.0f;  // a sum of weights up to this has none above it
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 
 template <int CH>  // channels of the operands: 64 or 128 (>= d)
@@ -71,8 +71,10 @@ struct Cfg {
   static constexpr int kToken = kRow + 16 + 2 + 1;  // bytes that a token brings
   static constexpr int kNumBars = 24;
   static constexpr int offMisc = offBar + kNumBars * 8;  // tensor memory base, abort flag, page masks [4]
-  static constexpr int offScratch = offMisc + 8 + 16;
+  static constexpr int offTop = offMisc + 8 + 16;  // [block % 4][expanding warp]: largest mu of its keys
+  static constexpr int offScratch = offTop + 64;
   static constexpr int kBytes = offScratch + (kThreads / 32 + 2) * 8;
+  static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
   // Tensor memory: S of tile q (P over its second half), then O.
   static __host__ __device__ constexpr uint32_t tS(int q) { return q * 128; }
   static __host__ __device__ constexpr uint32_t tO(int q) { return 256 + q * CH; }
@@ -182,8 +184,34 @@ __device__ __forceinline__ void expand_codes(uint32_t dst, uint32_t a, uint32_t 
   sts128(dst, x[0], x[1], x[2], x[3]);
 }
 
+// Sign words and scale mu of the rows of q: one warp per row, a channel per lane and word. (In the
+// attention kernel itself, 32 rows a warp, this took as long as two blocks for every (tile, head).)
+template <typename T>
+__global__ void __launch_bounds__(256) paged_q_kernel(PagedAttnParams p, uint4* bits, float* mu) {
+  allow_dependents();
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / 32;
+  const int lane = threadIdx.x & 31;
+  if (row >= p.T * p.heads) return;
+  const int64_t t = row / p.heads;
+  const T* src = static_cast<const T*>(p.q) + t * p.q_stride_t + (row - t * p.heads) * p.q_stride_h;
+  uint32_t word[4];
+  float sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float x = 32 * k + lane < p.cache.d ? load1<T>(src + 32 * k + lane) : 0.0f;
+    word[k] = __ballot_sync(0xffffffffu, x < 0.0f);
+    sum += fabsf(x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) {
+    bits[row] = make_uint4(word[0], word[1], word[2], word[3]);
+    mu[row] = sum / static_cast<float>(p.cache.d);
+  }
+}
+
 template <int CH>
-__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParams p, int q_f16, int unit, const __grid_constant__ CUtensorMap v_map) {
+__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParams p, int unit, const __grid_constant__ CUtensorMap v_map) {
   using C = Cfg<CH>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::offBar);
@@ -201,10 +229,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
       mbar_init(&bars[bVfull + i], 4);
       mbar_init(&bars[bKempty + i], 2);
       mbar_init(&bars[bVempty + i], 2);
+      mbar_init(&bars[bDrain + i], 1);
       mbar_init(&bars[bQfull + i], 4);
       mbar_init(&bars[bRead + i], 4);
       mbar_init(&bars[bPV + i], 1);
-      mbar_init(&bars[bDrain + i], 1);
       mbar_init(&bars[bP + i], 4);
       for (int h = 0; h < 2; ++h) mbar_init(&bars[bS + 2 * i + h], 1);
     }
@@ -358,6 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
         const uint4 bits = lds128(base + C::offBits + row * 16);
         const uint32_t mu = lds16(base + C::offMu + row * 2);
         const int e8 = static_cast<int8_t>(lds16(base + C::offExp + (row & ~1)) >> (8 * (row & 1)));
+        const uint32_t mu_top = __reduce_max_sync(0xffffffffu, mu);
+        if (lane == 0) *reinterpret_cast<volatile float*>(smem + C::offTop + (g & 3) * 16 + (warp - 4) * 4) = __uint_as_float(mu_top << 16);
         uint4 code[CH / 16];
 #pragma unroll
         for (int c = 0; c < CH / 16; ++c)
@@ -399,55 +429,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
     const uint32_t lane_base = static_cast<uint32_t>(w4 * 32) << 16;
     const uint32_t aS = tmem + lane_base + C::tS(q), aO = tmem + lane_base + C::tO(q);
     int g = 0, c = 0;
-    // Q of the (tile, head) `to` and the factor of its scores. The warp takes its rows one after the
-    // other, a channel per lane and word, and each lane keeps its own row's signs and sum. (Little code
-    // is what counts here: it runs once per (tile, head), when its instructions are not in any cache.)
+    // Q of the (tile, head) `to` and the factor of its scores, from what the preparation kernel left.
     auto write_q = [&](const Walk& to) {
-      uint32_t word[4] = {0u, 0u, 0u, 0u};
-      float total = 0.0f;
-      const int rows = min(32, to.w.rows - (r - lane));
-#pragma unroll 1
-      for (int r0 = 0; r0 < rows; r0 += 4) {
-        uint16_t raw[4][CH / 32];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int row = to.w.r0 + min(r - lane + r0 + u, to.w.rows - 1), i = p.by_group(row);
-          const uint16_t* src = static_cast<const uint16_t*>(p.q) + (to.w.t0 + i) * p.q_stride_t +
-                                (to.head * p.group + row - i * p.group) * p.q_stride_h;
-#pragma unroll
-          for (int x = 0; x < CH / 32; ++x) raw[u][x] = 32 * x + lane < cv.d ? __ldg(src + 32 * x + lane) : uint16_t{0};
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          float sum = 0.0f;
-          uint32_t neg[CH / 32];
-#pragma unroll
-          for (int x = 0; x < CH / 32; ++x) {
-            const float f = widen(raw[u][x], q_f16);
-            neg[x] = __ballot_sync(0xffffffffu, f < 0.0f);
-            sum += fabsf(f);
-          }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          if (lane == r0 + u) {
-            total = sum;
-#pragma unroll
-            for (int x = 0; x < CH / 32; ++x) word[x] = neg[x];
-          }
-        }
+      uint4 word = make_uint4(0u, 0u, 0u, 0u);
+      float mu = 0.0f;
+      if (r < to.w.rows) {
+        const int64_t at = out_row(p, to.w, to.head, r);
+        word = p.q_bits[at];
+        mu = p.q_mu[at];
       }
+      const uint32_t w4x[4] = {word.x, word.y, word.z, word.w};
       const uint32_t qd = base + C::offQ + q * C::kOp + (w4 * 32 + lane) * 16;
 #pragma unroll
       for (int i = 0; i < CH / 32; ++i) {
         const int n = cv.d - 32 * i;
-        if (n > 0) expand_signs(qd + i * 8192, word[i], 0x3f803f80u, low_bits(n));
+        if (n > 0) expand_signs(qd + i * 8192, w4x[i], 0x3f803f80u, low_bits(n));
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[bQfull + q]);
       // Above 0 also for a row of zeros, so that -inf in masked places stays -inf.
-      return fmaxf(p.scale_log2 * (total / static_cast<float>(cv.d)), 1e-30f);
+      return fmaxf(p.scale_log2 * mu, 1e-30f);
     };
+    grid_dependency_wait();  // for the rows of q
     bool ok = true, more = k.next(p);
     float cq_next = 1e-30f;
     if (!more && threadIdx.x == 8 * 32) p.notes[blockIdx.x].last = -1;  // nothing but the start of a cut one
@@ -455,8 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
     while (ok && more) {
       const RowTile w = k.w;
       const int head = k.head, n_blk = k.n_blk, v0 = k.v0, slot = k.slot;
-      const bool mine = q < k.tiles();
-      const int entry = k.entry, last_cta = k.last;
+      const bool mine = q < k.tiles();  // this (tile, head) has rows in the tile
+      if (threadIdx.x == 8 * 32) p.notes[blockIdx.x] = JoinNote{k.entry, head, k.last};  // the last one's stays
+      more = k.next(p);
+      const bool write_next = more && q < k.tiles() && k.n_blk > 0;
       const float cq = cq_next;
       const bool live = mine && r < w.rows;
       const int pos = w.pos0() + p.by_group(w.r0 + r);
@@ -499,6 +505,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
       auto arrived = [&](uint32_t (&s)[32]) {
         tmem_ld_wait();
         reg_fence32(s);
+      };
+      // Which of the keys j .. j + 31 the row sees.
+      auto seen = [&](int j, uint32_t pages) {
+        return low_bits(last - j + 1) & (~low_bits(wlo - j) | low_bits(p.sinks - j)) &
+               ((pages & 1u) * 0xffffu | (pages >> 1 & 1u) * 0xffff0000u);
+      };
+      auto mask = [&](uint32_t (&s)[32], uint32_t see) {
+        __syncwarp();  // keeps the callers' conditions branches
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (!((see >> i) & 1u)) s[i] = 0xff800000u;  // -inf
       };
       // Weights of 32 keys as 16 fp16 pairs; their sums are added to `sum`.
       auto weigh = [&](const uint32_t (&s)[32], uint32_t* to, float ref, float2 (&sum)[2]) {
@@ -549,6 +566,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
         if (again < 4) {
           float top = -CUDART_INF_F;
           uint32_t x[32];
+          // A mask alone needs no maximum where none can pass M by 2^15: |score| <= factor * d * mu.
+          const volatile float* most = reinterpret_cast<volatile float*>(smem + C::offTop + (g & 3) * 16);
+          const float mu_top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+          const bool known = __all_sync(0xffffffffu, !live || cq * static_cast<float>(cv.d) * mu_top <= M + kMostLog2);
           // Which of its 32 keys the row sees.
           auto seen = [&](int quarter) {
             const int j = j0 + 32 * quarter;
@@ -557,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
                    ((pages & 1u) * 0xffffu | (pages >> 1 & 1u) * 0xffff0000u);
           };
 #pragma unroll 1
-          for (int k = again; k < 4; ++k) {
+          for (int k = known ? 4 : again; k < 4; ++k) {
             read(32 * k, x);
             const uint32_t see = seen(k);
             arrived(x);
@@ -565,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
             for (int i = 0; i < 32; ++i) top = fmaxf(top, (see >> i) & 1u ? __uint_as_float(x[i]) : -CUDART_INF_F);
           }
           top *= cq;
-          if (__any_sync(0xffffffffu, top > M + kSlack)) {
+          if (!known && __any_sync(0xffffffffu, top > M + kSlack)) {
             const float f = move_to(top, n);
             if (!ok) break;
             if (again == 2) {  // the first half's weights, already fp16, are rounded once more
@@ -601,9 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
       }
       if (!ok) break;
       // The next (tile, head)'s scores can be made while this one's rows are written.
-      more = k.next(p);
-      if (more && q < k.tiles() && k.n_blk > 0) cq_next = write_q(k);
-      if (!more && threadIdx.x == 8 * 32) p.notes[blockIdx.x] = JoinNote{entry, head, last_cta};
+      if (write_next) cq_next = write_q(k);
       if (!mine) continue;
       // ------------------------------------------------------------ the rows' results
       if (n_blk > 0 && !(ok = wait_warp<false>(&bars[bPV + q], (c - 1) & 1, abort_flag))) break;
@@ -663,6 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
       }
     }
   }
+  grid_dependency_wait();  // also without work: this grid must not complete before the one before it
   tc_fence_before();
   named_barrier_sync(1, kThreads);
   if (warp == 0) {
@@ -680,8 +700,25 @@ cudaError_t launch_chunk(const PagedAttnParams& p, int dt, cudaStream_t s) {
   const int unit = v_unit(p.cache, kBlk);
   CUtensorMap map;
   if (!v_rows_map(p.cache, CH, unit, &map)) return cudaErrorInvalidValue;
-  paged_chunk_kernel<CH><<<p.ctas, kThreads, smem, s>>>(p, dt == BA_F16 ? 1 : 0, unit, map);
+  const unsigned q_grid = static_cast<unsigned>(ceil_div(p.T * p.heads, 8));
+  uint4* bits = const_cast<uint4*>(p.q_bits);
+  float* mu = const_cast<float*>(p.q_mu);
+  if (dt == BA_F16)
+    paged_q_kernel<__half><<<q_grid, 256, 0, s>>>(p, bits, mu);
+  else
+    paged_q_kernel<__nv_bfloat16><<<q_grid, 256, 0, s>>>(p, bits, mu);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, paged_chunk_kernel<CH>, p, unit, map)) != cudaSuccess) return e;
   return launch_line_join(p, kBlk, s);
 }
 

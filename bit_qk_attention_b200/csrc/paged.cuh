@@ -80,6 +80,8 @@ struct PagedAttnParams {
   int ctas;          // CTAs that share the line of units; 0: a cluster of CTAs per (tile, head)
   int cluster;       // its size
   JoinNote* notes;   // [ctas]
+  const uint4* q_bits;  // [T * heads] sign words of q (many rows)
+  const float* q_mu;    // [T * heads] their scales
 };
 
 // What a CTA works on: a tile of rows r = i * group + g (i-th new token, g-th head of the group) of
