@@ -13,7 +13,7 @@ using namespace binattn;
 
 namespace {
 
-constexpr int64_t kMaxRows = int64_t{1} << 31;  // (token, head) rows of a call
+constexpr int64_t kMaxRows = (int64_t{1} << 31) - 4096;  // (token, head) rows of a call
 constexpr int64_t kMaxKv = int64_t{1} << 28;
 // Rows (new tokens x heads of a group) per sequence up to which the decoding kernel is taken.
 constexpr int kDecodeRows = 32;
@@ -57,9 +57,9 @@ size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // Regions of the workspace of a launch whose CTAs share the line of units; their size in bytes.
 size_t line_workspace(const PagedAttnParams& p, PagedAttnParams* out) {
-  const size_t n = static_cast<size_t>(p.ctas) * 2 * p.row_tile;
+  const size_t ctas = p.whole ? 0 : p.ctas, n = ctas * 2 * p.row_tile;
   const size_t ml = align_up(n * p.cache.dp * 4), notes = ml + align_up(n * 8);
-  const size_t bits = notes + align_up(static_cast<size_t>(p.ctas) * sizeof(JoinNote));
+  const size_t bits = notes + align_up(ctas * sizeof(JoinNote));
   const size_t rows = p.row_tile == kChunkRows ? static_cast<size_t>(p.T) * p.heads : 0, mu = bits + align_up(rows * 16);
   if (out != nullptr) {
     char* base = reinterpret_cast<char*>(out->part_o);
@@ -148,6 +148,8 @@ ba_status ba_cache_write(const void* k, int64_t k_stride_t, int64_t k_stride_h, 
   p.slots = slots;
   p.wide = cache->d % 8 == 0 && aligned(k, 16) && aligned(v, 16) &&
            (k_stride_t | k_stride_h | v_stride_t | v_stride_h) % 8 == 0;
+  p.by_heads = FastDiv::of(cache->n_kv_heads);
+  p.by_page = FastDiv::of(cache->page_size);
   return report_cuda(launch_cache_write(p, dt, static_cast<cudaStream_t>(stream)));
 }
 
@@ -166,6 +168,8 @@ ba_status ba_cache_read(const ba_kv_cache* cache, const int64_t* slots, int64_t 
   p.T = T;
   p.k = k;
   p.v = v;
+  p.by_heads = FastDiv::of(cache->n_kv_heads);
+  p.by_page = FastDiv::of(cache->page_size);
   return report_cuda(launch_cache_read(p, dt, static_cast<cudaStream_t>(stream)));
 }
 

@@ -49,6 +49,7 @@ using namespace ptx;
 constexpr int kBlk = 128;      // keys per block: N of QK, K of PV
 constexpr int kTile = 128;     // rows per tile: M
 constexpr int kCost = 2;       // blocks that a CTA could do while it starts and ends a (tile, head)
+constexpr int kWholeBlocks = 6;  // blocks that cutting a (tile, head) has to save
 constexpr int kMinUnits = 4;   // units (blocks, and kCost) a CTA takes at least
 constexpr int kThreads = 512;  // service, expanding and two softmax warpgroups
 constexpr float kSlack = 8.0f;        // log2 by which a block's maximum may pass M
@@ -247,7 +248,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
     tmem_relinquish();
   }
   Walk k;
-  k.line = find_stretch<kThreads>(p, kBlk, kCost, kMinUnits, reinterpret_cast<int64_t*>(smem + C::offScratch));
+  if (p.whole) {  // one (tile, head) per CTA
+    const int entry = p.by_kv_heads(blockIdx.x), units = units_of(entry_tile(p, entry, kBlk), kCost);
+    const int64_t at = static_cast<int64_t>(blockIdx.x - entry * cv.heads) * units;
+    k.line = Stretch{at, at + units, 0, units, entry};
+  } else {
+    k.line = find_stretch<kThreads>(p, kBlk, kCost, kMinUnits, reinterpret_cast<int64_t*>(smem + C::offScratch));
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -454,13 +461,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
     grid_dependency_wait();  // for the rows of q
     bool ok = true, more = k.next(p);
     float cq_next = 1e-30f;
-    if (!more && threadIdx.x == 8 * 32) p.notes[blockIdx.x].last = -1;  // nothing but the start of a cut one
+    if (!more && threadIdx.x == 8 * 32 && !p.whole) p.notes[blockIdx.x].last = -1;  // nothing but the start of a cut one
     if (more && q < k.tiles() && k.n_blk > 0) cq_next = write_q(k);
     while (ok && more) {
       const RowTile w = k.w;
       const int head = k.head, n_blk = k.n_blk, v0 = k.v0, slot = k.slot;
       const bool mine = q < k.tiles();  // this (tile, head) has rows in the tile
-      if (threadIdx.x == 8 * 32) p.notes[blockIdx.x] = JoinNote{k.entry, head, k.last};  // the last one's stays
+      if (threadIdx.x == 8 * 32 && !p.whole) p.notes[blockIdx.x] = JoinNote{k.entry, head, k.last};  // the last one's stays
       more = k.next(p);
       const bool write_next = more && q < k.tiles() && k.n_blk > 0;
       const float cq = cq_next;
@@ -719,7 +726,7 @@ cudaError_t launch_chunk(const PagedAttnParams& p, int dt, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, paged_chunk_kernel<CH>, p, unit, map)) != cudaSuccess) return e;
-  return launch_line_join(p, kBlk, s);
+  return p.whole ? cudaSuccess : launch_line_join(p, kBlk, s);
 }
 
 }  // namespace
@@ -734,7 +741,11 @@ void paged_chunk_plan(PagedAttnParams* p, int sms) {
     keys = std::min<int64_t>(keys, static_cast<int64_t>(p->window) + p->row_tile / p->group + p->sinks + 2 * kBlk);
   const int64_t blocks = ceil_div(keys, kBlk), tiles = static_cast<int64_t>(p->B) * p->row_tiles * p->cache.heads;
   p->cluster = 1;
-  p->ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, (blocks + kCost) * tiles / kMinUnits)));
+  // Cutting (tile, head)s to fill the GPU costs what kWholeBlocks blocks do (finding the cuts, and the
+  // second launch): 80 of 12 blocks took 41 us whole and 49 us cut, 80 of 16 blocks 52 us either way.
+  const int64_t even = std::max<int64_t>((blocks + kCost) * tiles / sms, kMinUnits - kCost);
+  p->whole = tiles <= sms && blocks - even <= kWholeBlocks ? 1 : 0;
+  p->ctas = p->whole ? static_cast<int>(tiles) : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, (blocks + kCost) * tiles / kMinUnits)));
 }
 
 cudaError_t read_and_clear_chunk_status(int* value, cudaStream_t s) {

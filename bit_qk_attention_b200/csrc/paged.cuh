@@ -22,24 +22,6 @@ struct CacheView {
   __device__ uint8_t* block(int64_t page, int head) const { return data + (page * heads + head) * block_bytes; }
 };
 
-struct CacheWriteParams {
-  CacheView cache;
-  const void* k;
-  const void* v;
-  int64_t k_stride_t, k_stride_h, v_stride_t, v_stride_h;  // elements
-  int64_t T;
-  const int64_t* slots;
-  bool wide;  // every row of k and v starts on 16 bytes and d is a multiple of 8
-};
-
-struct CacheReadParams {
-  CacheView cache;
-  const int64_t* slots;
-  int64_t T;
-  void* k;
-  void* v;
-};
-
 // n / d for 0 <= n < 2^31, without a division: mul = ceil(2^(31 + s) / d) with 2^(s-1) < d <= 2^s is
 // off by less than 2^s / 2^(31 + s) of the quotient's scale, too little to reach the next whole number.
 struct FastDiv {
@@ -53,6 +35,34 @@ struct FastDiv {
     return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> shift);
   }
 };
+
+struct CacheWriteParams {
+  CacheView cache;
+  const void* k;
+  const void* v;
+  int64_t k_stride_t, k_stride_h, v_stride_t, v_stride_h;  // elements
+  int64_t T;
+  const int64_t* slots;
+  bool wide;  // every row of k and v starts on 16 bytes and d is a multiple of 8
+  FastDiv by_heads, by_page;
+};
+
+struct CacheReadParams {
+  CacheView cache;
+  const int64_t* slots;
+  int64_t T;
+  void* k;
+  void* v;
+  FastDiv by_heads, by_page;
+};
+
+// Page of a slot and the offset in it; page -1 outside the cache.
+__device__ __forceinline__ int64_t page_of_slot(const CacheView& cv, const FastDiv& by_page, int64_t slot, int& off) {
+  if (slot < 0 || slot >= cv.num_pages * cv.page_size) return -1;
+  const int64_t page = (slot >> 31) == 0 ? by_page(static_cast<int>(slot)) : slot / cv.page_size;
+  off = static_cast<int>(slot - page * cv.page_size);
+  return page;
+}
 
 // Attention of new tokens over the cache.
 struct JoinNote;
@@ -79,6 +89,7 @@ struct PagedAttnParams {
   float2* part_ml;   // [ctas][2][row_tile] (maximum in log2, sum)
   int ctas;          // CTAs that share the line of units; 0: a cluster of CTAs per (tile, head)
   int cluster;       // its size
+  int whole;         // many rows: each CTA has one (tile, head), nothing is cut
   JoinNote* notes;   // [ctas]
   const uint4* q_bits;  // [T * heads] sign words of q (many rows)
   const float* q_mu;    // [T * heads] their scales
