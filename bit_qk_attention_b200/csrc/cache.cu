@@ -7,8 +7,14 @@
 // A half-warp takes a row of one head at a time, eight channels per lane: 16-byte loads of k and v, one
 // sign byte and eight code bytes per lane, so that a row's 16 sign bytes and its codes leave as one
 // piece each. The two reductions (sum |k|, max |v|) are four shuffles each. Neighbouring half-warps take
-// neighbouring heads of a token, whose rows lie next to each other in k and v, and each has several
-// rows in flight (kRows): with one, a thread asks for too few bytes to cover the memory's latency.
+// neighbouring heads of a token, whose rows lie next to each other in k and v. (Two, four or eight rows
+// in flight per half-warp were no faster on large calls and slower on small ones; so was a half-warp's
+// neighbour taking the next token of the same head.) Stores of read rows are streaming: they are as
+// large as all of L2 on long contexts.
+//
+// 16384 tokens x 8 heads x 128 channels (d): written in 20 us (4.3 TB/s; a third of the bytes are small
+// pieces of pages in any order), read in 14 us (6.2 TB/s, all from L2); 65536 tokens read in 72 to 78
+// us (4.4 to 4.8 TB/s); 8 tokens of 16 heads 1.8 us each way, of which a launch alone is most.
 #include "kernels.h"
 #include "paged.cuh"
 
@@ -18,8 +24,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kLanes = 16;  // lanes of a row
-constexpr int kRows = 4;    // rows of a half-warp, kHalves apart
-constexpr int kHalves = kThreads / kLanes;
+constexpr int kHalves = kThreads / kLanes;  // rows of a CTA
 
 // The least e with amax <= 127 * 2^e, held to [kMinExp, kMaxExp]. amax = f * 2^x with
 // 1 <= f < 2 gives x - 6 when f <= 127/64 (mantissa bits up to 0x7e0000), else x - 5. Zero and
@@ -31,69 +36,71 @@ __device__ __forceinline__ int row_exp(float amax) {
   return min(max(e, kMinExp), kMaxExp);
 }
 
+// Eight channels of a row of k or v as they come (channels from d on are 0).
 template <typename T, bool WIDE>
-__device__ __forceinline__ void load_row8(const T* row, int c0, int d, float f[8]) {
+__device__ __forceinline__ uint4 load_row8(const T* row, int c0, int d) {
+  uint4 u = make_uint4(0u, 0u, 0u, 0u);
   if (WIDE) {
-    uint4 u = make_uint4(0u, 0u, 0u, 0u);
     if (c0 < d) u = ldg_stream(row + c0);
-    unpack8<T>(u, f);
   } else {
+    const uint16_t* x = reinterpret_cast<const uint16_t*>(row);
+    uint32_t* w = reinterpret_cast<uint32_t*>(&u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = c0 + i < d ? load1<T>(row + c0 + i) : 0.0f;
+    for (int i = 0; i < 8; ++i)
+      if (c0 + i < d) w[i / 2] |= static_cast<uint32_t>(__ldg(x + c0 + i)) << (16 * (i % 2));
   }
+  return u;
 }
 
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheWriteParams p) {
   const CacheView& cv = p.cache;
-  const int c0 = (threadIdx.x % kLanes) * 8, rows = static_cast<int>(p.T) * cv.heads;
-  const int first = blockIdx.x * (kHalves * kRows) + threadIdx.x / kLanes;
-  float k[kRows][8], v[kRows][8];
-  uint8_t* blk[kRows];
-  int off[kRows];
+  const int c0 = (threadIdx.x % kLanes) * 8, row = blockIdx.x * kHalves + threadIdx.x / kLanes;
   // Every lane stays for the shuffles; lanes of a row that is not written load nothing.
+  const bool in = row < static_cast<int>(p.T) * cv.heads;
+  const int t = in ? p.by_heads(row) : 0, h = in ? row - t * cv.heads : 0;
+  int off = 0;
+  const int64_t page = in ? page_of_slot(cv, p.by_page, p.slots[t], off) : -1;
+  const int d = page >= 0 ? cv.d : 0;
+  float k[8], v[8];
+  unpack8<T>(load_row8<T, WIDE>(static_cast<const T*>(p.k) + t * p.k_stride_t + h * p.k_stride_h, c0, d), k);
+  unpack8<T>(load_row8<T, WIDE>(static_cast<const T*>(p.v) + t * p.v_stride_t + h * p.v_stride_h, c0, d), v);
+  uint32_t neg = 0;
+  float sum = 0.0f, amax = 0.0f;
 #pragma unroll
-  for (int u = 0; u < kRows; ++u) {
-    const int row = first + u * kHalves, t = row < rows ? p.by_heads(row) : 0, h = row < rows ? row - t * cv.heads : 0;
-    const int64_t page = row < rows ? page_of_slot(cv, p.by_page, p.slots[t], off[u]) : -1;
-    blk[u] = page >= 0 ? cv.block(page, h) : nullptr;
-    const int d = page >= 0 ? cv.d : 0;
-    load_row8<T, WIDE>(static_cast<const T*>(p.k) + t * p.k_stride_t + h * p.k_stride_h, c0, d, k[u]);
-    load_row8<T, WIDE>(static_cast<const T*>(p.v) + t * p.v_stride_t + h * p.v_stride_h, c0, d, v[u]);
+  for (int i = 0; i < 8; ++i) {
+    neg |= (k[i] < 0.0f ? 1u : 0u) << i;
+    sum += fabsf(k[i]);
+    amax = fmaxf(amax, fabsf(v[i]));
   }
 #pragma unroll
-  for (int u = 0; u < kRows; ++u) {
-    uint32_t neg = 0;
-    float sum = 0.0f, amax = 0.0f;
+  for (int o = kLanes / 2; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  }
+  if (page < 0) return;
+  uint8_t* blk = cv.block(page, h);
+  blk[cv.off_bits() + off * 16 + c0 / 8] = static_cast<uint8_t>(neg);
+  const int e = row_exp(amax);
+  if (c0 == 0) {
+    *reinterpret_cast<__nv_bfloat16*>(blk + cv.off_mu() + off * 2) = __float2bfloat16_rn(sum / static_cast<float>(cv.d));
+    *reinterpret_cast<int8_t*>(blk + cv.off_exp() + off) = static_cast<int8_t>(e);
+  }
+  if (c0 < cv.dp) {
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e: v * inv is exact
+    if (e == kMaxExp) {  // only there can a value lie beyond 127 steps
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      neg |= (k[u][i] < 0.0f ? 1u : 0u) << i;
-      sum += fabsf(k[u][i]);
-      amax = fmaxf(amax, fabsf(v[u][i]));
+      for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -127.0f * 512.0f), 127.0f * 512.0f);
     }
+    // v * inv + 1.5 * 2^23 rounds to the nearest whole number, ties to even, in the low bits.
+    uint32_t q[8], w[2];
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) {
-      sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    }
-    if (blk[u] == nullptr) continue;
-    blk[u][cv.off_bits() + off[u] * 16 + c0 / 8] = static_cast<uint8_t>(neg);
-    const int e = row_exp(amax);
-    if (c0 == 0) {
-      *reinterpret_cast<__nv_bfloat16*>(blk[u] + cv.off_mu() + off[u] * 2) =
-          __float2bfloat16_rn(sum / static_cast<float>(cv.d));
-      *reinterpret_cast<int8_t*>(blk[u] + cv.off_exp() + off[u]) = static_cast<int8_t>(e);
-    }
-    if (c0 < cv.dp) {
-      const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e: v * inv is exact
-      uint32_t w[2] = {0u, 0u};
+    for (int i = 0; i < 8; ++i) q[i] = __float_as_uint(__fmaf_rn(v[i], inv, 12582912.0f));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int q = min(127, max(-127, __float2int_rn(v[u][i] * inv)));
-        w[i / 4] |= (static_cast<uint32_t>(q) & 0xffu) << (8 * (i % 4));
-      }
-      *reinterpret_cast<uint2*>(blk[u] + off[u] * cv.dp + c0) = make_uint2(w[0], w[1]);
-    }
+    for (int i = 0; i < 2; ++i)
+      w[i] = __byte_perm(__byte_perm(q[4 * i], q[4 * i + 1], 0x0040), __byte_perm(q[4 * i + 2], q[4 * i + 3], 0x0040),
+                         0x5410);
+    *reinterpret_cast<uint2*>(blk + off * cv.dp + c0) = make_uint2(w[0], w[1]);
   }
 }
 
@@ -115,7 +122,7 @@ __device__ __forceinline__ void store_row8(T* row, int c0, int d, const float f[
     for (int i = 0; i < 8; ++i) out[i] = narrow<T>(f[i]);
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(out) / 16); ++i)
-      reinterpret_cast<uint4*>(row + c0)[i] = reinterpret_cast<const uint4*>(out)[i];
+      __stcs(reinterpret_cast<uint4*>(row + c0) + i, reinterpret_cast<const uint4*>(out)[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -126,49 +133,38 @@ __device__ __forceinline__ void store_row8(T* row, int c0, int d, const float f[
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheReadParams p) {
   const CacheView& cv = p.cache;
-  const int c0 = (threadIdx.x % kLanes) * 8, rows = static_cast<int>(p.T) * cv.heads;
-  const int first = blockIdx.x * (kHalves * kRows) + threadIdx.x / kLanes;
-  if (c0 >= cv.d) return;
-  uint32_t neg[kRows];
-  float mu[kRows], step[kRows];
-  uint2 code[kRows];
-#pragma unroll
-  for (int u = 0; u < kRows; ++u) {
-    const int row = first + u * kHalves, t = row < rows ? p.by_heads(row) : 0;
-    int off = 0;
-    const int64_t page = row < rows ? page_of_slot(cv, p.by_page, p.slots[t], off) : -1;
-    neg[u] = 0;
-    mu[u] = step[u] = 0.0f;
-    code[u] = make_uint2(0u, 0u);
-    if (page >= 0) {
-      const uint8_t* blk = cv.block(page, row - t * cv.heads);
-      neg[u] = blk[cv.off_bits() + off * 16 + c0 / 8];
-      mu[u] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(blk + cv.off_mu() + off * 2));
-      step[u] = ldexpf(1.0f, *reinterpret_cast<const int8_t*>(blk + cv.off_exp() + off));
-      code[u] = *reinterpret_cast<const uint2*>(blk + off * cv.dp + c0);
-    }
+  const int c0 = (threadIdx.x % kLanes) * 8, row = blockIdx.x * kHalves + threadIdx.x / kLanes;
+  if (row >= static_cast<int>(p.T) * cv.heads || c0 >= cv.d) return;
+  const int t = p.by_heads(row);
+  int off = 0;
+  const int64_t page = page_of_slot(cv, p.by_page, p.slots[t], off);
+  uint32_t neg = 0;
+  float mu = 0.0f, step = 0.0f;
+  uint2 code = make_uint2(0u, 0u);
+  if (page >= 0) {
+    const uint8_t* blk = cv.block(page, row - t * cv.heads);
+    neg = blk[cv.off_bits() + off * 16 + c0 / 8];
+    mu = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(blk + cv.off_mu() + off * 2));
+    const int e = *reinterpret_cast<const int8_t*>(blk + cv.off_exp() + off);
+    step = __uint_as_float(static_cast<uint32_t>(127 + max(e, -126)) << 23);
+    code = *reinterpret_cast<const uint2*>(blk + off * cv.dp + c0);
   }
+  const int64_t at = static_cast<int64_t>(row) * cv.d;
+  float f[8];
+  if (p.k != nullptr) {
 #pragma unroll
-  for (int u = 0; u < kRows; ++u) {
-    const int row = first + u * kHalves;
-    if (row >= rows) return;
-    const int64_t at = static_cast<int64_t>(row) * cv.d;
-    float f[8];
-    if (p.k != nullptr) {
+    for (int i = 0; i < 8; ++i) f[i] = (neg >> i) & 1u ? -mu : mu;
+    store_row8<T, WIDE>(static_cast<T*>(p.k) + at, c0, cv.d, f);
+  }
+  if (p.v != nullptr) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = (neg[u] >> i) & 1u ? -mu[u] : mu[u];
-      store_row8<T, WIDE>(static_cast<T*>(p.k) + at, c0, cv.d, f);
-    }
-    if (p.v != nullptr) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        f[i] = static_cast<float>(static_cast<int8_t>((i < 4 ? code[u].x : code[u].y) >> (8 * (i % 4)))) * step[u];
-      store_row8<T, WIDE>(static_cast<T*>(p.v) + at, c0, cv.d, f);
-    }
+    for (int i = 0; i < 8; ++i)
+      f[i] = static_cast<float>(static_cast<int8_t>((i < 4 ? code.x : code.y) >> (8 * (i % 4)))) * step;
+    store_row8<T, WIDE>(static_cast<T*>(p.v) + at, c0, cv.d, f);
   }
 }
 
-unsigned grid_for(int64_t rows) { return static_cast<unsigned>(ceil_div(rows, kHalves * kRows)); }
+unsigned grid_for(int64_t rows) { return static_cast<unsigned>(ceil_div(rows, kHalves)); }
 
 template <typename T>
 cudaError_t launch_write(const CacheWriteParams& p, cudaStream_t s) {
