@@ -395,7 +395,7 @@ class KVCache:
 
     def c(self) -> CKvCache:
         t = self._data
-        if self._c is None:
+        if self._c is None or self._c.data != t.data_ptr():
             if t.dtype != _torch().uint8 or t.dim() != 3 or not t.is_cuda or not t.is_contiguous():
                 raise ValueError("cache data must be a contiguous uint8 CUDA tensor [pages, heads, block bytes]")
             if t.shape[2] != kv_block_bytes(self._page_size, self._d) or t.shape[2] == 0:
@@ -537,6 +537,9 @@ def attention_paged(q, cache: KVCache, page_table, kv_lens, cu_seqlens_q=None, m
         odt = dt if out_dtype is None else _dt(out)
     lse = q.new_empty((T, heads), dtype=torch.float32) if return_lse else None
     L = lib()
+    # Larger numbers than a C int holds mean the same as the largest.
+    max_q_len, window, sinks = min(max_q_len, 0x7fffffff), min(window, 0x7fffffff), min(sinks, 0x7fffffff)
+    max_kv_len = min(max_kv_len, pages * cc.page_size)
     sq = CPagedSeqs(B, T, heads, max_q_len, max_kv_len, cu, kv_lens.data_ptr(), page_table.data_ptr(),
                     page_table.stride(0), pages, 1 if causal else 0, window, sinks)
     c_cache, c_seqs = ctypes.byref(cc), ctypes.byref(sq)
@@ -545,8 +548,8 @@ def attention_paged(q, cache: KVCache, page_table, kv_lens, cu_seqlens_q=None, m
         # (size_t) -1 stands for arguments that the call below refuses.
         if 0 < nws != ctypes.c_size_t(-1).value:
             workspace = kv_lens.new_empty((nws,), dtype=torch.uint8)
-    elif workspace.get_device() != dev:
-        raise ValueError("workspace must be on the cache's device")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
     qt, qh, _ = q.stride()
     _check(L.ba_attention_paged(q.data_ptr(), qt, qh, dt, c_cache, c_seqs, softmax_scale, out.data_ptr(), odt,
                                 0 if lse is None else lse.data_ptr(), 0 if workspace is None else workspace.data_ptr(),

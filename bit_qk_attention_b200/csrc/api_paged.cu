@@ -15,8 +15,19 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t{1} << 31) - 4096;  // (token, head) rows of a call
 constexpr int64_t kMaxKv = int64_t{1} << 28;
-// Rows (new tokens x heads of a group) per sequence up to which the decoding kernel is taken.
-constexpr int kDecodeRows = 32;
+// Rows (new tokens x heads of a group) of a sequence up to which the decoding kernel is taken, with a
+// pass over the cache for every 16 rows (8 KV heads, d = 128, decoding kernel and the other one, us):
+//              1 x 8192 keys  32 x 4096  128 x 1024
+//   16 rows       18   41       49  186    79  194
+//   32 rows       19   42      101  186   140  195
+//   48 rows       20   42      141  187   199  199
+//   64 rows       23   42      180  187   260  200
+constexpr int kDecodeRows = 48;
+// Up to so many where its tiles fit on the GPU at once and a warp has at most so many blocks of 64 keys:
+// there the other kernel's start, cuts and join last longer than the further passes. 128 rows: 1 x 8192
+// keys (7 blocks) 30 and 44 us; 4 heads of 2 x 16384 (14 blocks) 48 and 57; 8 heads of 1 x 65536 (55
+// blocks) 149 and 100. 64 rows, 16 x 1024 keys, twice as many tiles as fit: 48 and 30.
+constexpr int kDraftRows = 128, kDraftBlocks = 24;
 constexpr int kChunkRows = 256;  // row tile of the kernel for more
 constexpr int64_t kMaxCtas = (int64_t{1} << 31) - 1;
 
@@ -96,11 +107,16 @@ ba_status plan(const ba_kv_cache* cache, const ba_paged_seqs* s, PagedAttnParams
   p->table = s->page_table;
   p->table_stride = s->table_stride;
   p->causal = s->causal;
-  p->window = s->window;
-  p->sinks = s->sinks;
+  // Positions lie within +-2^28: longer windows and more sinks hide nothing either, and sums with these
+  // stay within an int.
+  p->window = static_cast<int>(std::min<int64_t>(s->window, 2 * kMaxKv));
+  p->sinks = static_cast<int>(std::min<int64_t>(s->sinks, kMaxKv));
   if (p->B == 0 || p->max_q_len == 0) return BA_OK;  // nothing to launch
   const int64_t rows = static_cast<int64_t>(p->max_q_len) * p->group;
-  p->row_tile = rows <= 8 ? 8 : (rows <= kDecodeRows ? 16 : kChunkRows);
+  const int64_t tiles16 = ceil_div(rows, 16) * p->B * p->cache.heads, at_once = 2 * sm_count();
+  const bool few = rows <= kDecodeRows || (rows <= kDraftRows && tiles16 <= at_once &&
+                                           tiles16 * most_blocks(*p, 16, 64) <= at_once * 4 * kDraftBlocks);
+  p->row_tile = rows <= 8 ? 8 : (few ? 16 : kChunkRows);
   const int64_t tiles = ceil_div(rows, p->row_tile);
   if (tiles > kMaxCtas / (static_cast<int64_t>(p->B) * p->cache.heads)) return BA_ERR_UNSUPPORTED;
   p->row_tiles = static_cast<int>(tiles);
@@ -108,7 +124,9 @@ ba_status plan(const ba_kv_cache* cache, const ba_paged_seqs* s, PagedAttnParams
   p->by_kv_heads = FastDiv::of(p->cache.heads);
   p->by_page = FastDiv::of(p->cache.page_size);
   p->by_tiles = FastDiv::of(p->row_tiles);
-  if (tiles * p->B * p->cache.heads > kMaxCtas / p->row_tile) return BA_ERR_UNSUPPORTED;
+  const int64_t all = tiles * p->B * p->cache.heads;
+  // Row slots count in 31 bits, and so does a CTA's share of the key blocks (64 or 128 keys).
+  if (all > kMaxCtas / p->row_tile || all > (int64_t{1} << 38) / (p->max_kv_len / 64 + 16)) return BA_ERR_UNSUPPORTED;
   if (p->row_tile == kChunkRows)
     paged_chunk_plan(p, sm_count());
   else

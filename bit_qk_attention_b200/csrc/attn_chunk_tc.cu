@@ -393,7 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
         const uint4 bits = lds128(base + C::offBits + row * 16);
         const uint32_t mu = lds16(base + C::offMu + row * 2);
         const int e8 = static_cast<int8_t>(lds16(base + C::offExp + (row & ~1)) >> (8 * (row & 1)));
-        const uint32_t mu_top = __reduce_max_sync(0xffffffffu, mu);
+        // A row behind the sequence may hold a negative mu: its sign would hide the others.
+        const uint32_t mu_top = __reduce_max_sync(0xffffffffu, mu & 0x7fffu);
         if (lane == 0) *reinterpret_cast<volatile float*>(smem + C::offTop + (g & 3) * 16 + (warp - 4) * 4) = __uint_as_float(mu_top << 16);
         uint4 code[CH / 16];
 #pragma unroll
@@ -412,8 +413,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
         if (lane == 0) mbar_arrive(&bars[bKfull + st]);
         if (g >= 2 && !(ok = wait_warp<true>(&bars[bVempty + st], ((g >> 1) - 1) & 1, abort_flag))) break;
         const uint32_t vd = base + C::offV + st * C::kOp + row * 16;
-        // A row behind the sequence may hold anything: times 0 it is finite, as its weight of 0 needs.
-        const bool in = k.w.block_at(k.v0 + n) * kBlk + row < k.w.kv;
+        // A row that no query row sees may hold anything: times 0 it is finite, as its weight of 0 needs.
+        const int j = k.w.block_at(k.v0 + n) * kBlk + row;
+        const bool in = j < k.w.kv && (j >= k.w.lo || j < p.sinks);
         const __half2 step = __float2half2_rn(
             in ? __uint_as_float(static_cast<uint32_t>(127 + min(max(e8, kMinExp), kMaxExp)) << 23) : 0.0f);
 #pragma unroll
@@ -736,10 +738,7 @@ cudaError_t launch_paged_chunk(const PagedAttnParams& p, int dt, cudaStream_t s)
 }
 
 void paged_chunk_plan(PagedAttnParams* p, int sms) {
-  int64_t keys = p->max_kv_len;
-  if (p->causal && p->window > 0)
-    keys = std::min<int64_t>(keys, static_cast<int64_t>(p->window) + p->row_tile / p->group + p->sinks + 2 * kBlk);
-  const int64_t blocks = ceil_div(keys, kBlk), tiles = static_cast<int64_t>(p->B) * p->row_tiles * p->cache.heads;
+  const int64_t blocks = most_blocks(*p, p->row_tile, kBlk), tiles = static_cast<int64_t>(p->B) * p->row_tiles * p->cache.heads;
   p->cluster = 1;
   // Cutting (tile, head)s to fill the GPU costs what kWholeBlocks blocks do (finding the cuts, and the
   // second launch): 80 of 12 blocks took 41 us whole and 49 us cut, 80 of 16 blocks 52 us either way.

@@ -102,6 +102,7 @@ struct RowTile {
   int64_t t0;     // row of q of the sequence's first new token
   int nq, kv;     // new tokens, tokens in the cache
   int r0, rows;   // first row of the tile, rows in it (<= 0: nothing to do)
+  int lo;         // no row sees keys below it, but for the sinks
   int nsink, first, nblk;  // sink blocks, first block after them, blocks in all
 
   __device__ int block_at(int v) const { return v < nsink ? v : first + (v - nsink); }
@@ -128,10 +129,17 @@ __device__ __forceinline__ RowTile row_tile(const PagedAttnParams& p, int b, int
     hi = min(hi, w.pos0() + p.by_group(w.r0 + w.rows - 1) + 1);
     if (p.window > 0) lo = max(0, w.pos0() + p.by_group(w.r0) - p.window + 1);
   }
+  w.lo = lo;
   w.first = lo / bk;
   w.nsink = min(static_cast<int>(ceil_div(p.sinks, bk)), w.first);
   w.nblk = hi <= 0 || w.rows <= 0 ? 0 : w.nsink + static_cast<int>(ceil_div(hi, bk)) - w.first;
   return w;
+}
+
+// Row of o (and of lse) of the tile's row r.
+__device__ __forceinline__ int64_t out_row(const PagedAttnParams& p, const RowTile& w, int head, int r) {
+  const int i = p.by_group(w.r0 + r);
+  return (w.t0 + i) * p.heads + head * p.group + (w.r0 + r - i * p.group);
 }
 
 // The work of a launch is a line of units, for all sequences' row tiles, one KV head after the other:
@@ -140,12 +148,6 @@ __device__ __forceinline__ RowTile row_tile(const PagedAttnParams& p, int b, int
 // may be cut at the ends of CTAs. What a CTA computes of a cut one goes into the workspace: slot 0 if
 // it began before the CTA, else slot 1. The CTA in which a cut one begins leaves a note for the
 // kernel that joins the parts.
-// Row of o (and of lse) of the tile's row r.
-__device__ __forceinline__ int64_t out_row(const PagedAttnParams& p, const RowTile& w, int head, int r) {
-  const int i = p.by_group(w.r0 + r);
-  return (w.t0 + i) * p.heads + head * p.group + (w.r0 + r - i * p.group);
-}
-
 struct JoinNote {
   int entry, head;  // entry = b * row_tiles + tile
   int last;         // CTA with the last part; the CTAs between have it in slot 0. -1: nothing to join
@@ -248,6 +250,16 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// Key blocks of bk tokens that a tile of `rows` rows can see, at most.
+inline int64_t most_blocks(const PagedAttnParams& p, int rows, int bk) {
+  int64_t keys = p.max_kv_len;
+  if (p.causal && p.window > 0) {
+    const int64_t near = static_cast<int64_t>(p.window) + rows / p.group + p.sinks + 2 * bk;
+    keys = keys < near ? keys : near;
+  }
+  return ceil_div(keys, bk);
 }
 
 cudaError_t launch_paged_decode(const PagedAttnParams& p, int dt, cudaStream_t s);

@@ -270,7 +270,7 @@ def test_without_causal_mask(ba, shape):
     _compare(*_run(ba, prob, causal=False), _ref(ba, prob, causal=False))
 
 
-@pytest.mark.parametrize("qn", [[1, 1, 1], [2, 4, 40], [70, 5, 150]])
+@pytest.mark.parametrize("qn", [[1, 1, 1], [2, 4, 40], [40, 5, 64], [70, 5, 150]])
 def test_rows_that_see_nothing(ba, qn):
     """More new tokens than the cache holds: the first ones are before the first key. Also an empty cache."""
     kn = [0, 3, 30]
@@ -298,7 +298,7 @@ def test_large_scores(ba, scale, lean, qn):
     _compare(*_run(ba, prob, softmax_scale=scale), _ref(ba, prob, softmax_scale=scale))
 
 
-@pytest.mark.parametrize("qn", [[1], [64]])
+@pytest.mark.parametrize("qn", [[1], [64], [100]])
 def test_values_of_very_different_size(ba, qn):
     """One key's values are 2^30 times another's; zero rows have the least exponent and weigh as much as any."""
     d, ps, n = 64, 16, 200
@@ -314,7 +314,7 @@ def test_values_of_very_different_size(ba, qn):
     _compare(*_run(ba, prob), _ref(ba, prob))
 
 
-@pytest.mark.parametrize("qn,causal", [([1, 1], True), ([30, 50], True), ([1, 40], False)])
+@pytest.mark.parametrize("qn,causal", [([1, 1], True), ([30, 50], True), ([1, 40], False), ([70, 30], True), ([2, 80], False)])
 def test_missing_pages_and_garbage_outside_the_sequences(ba, qn, causal):
     """Tokens on pages outside the cache are not seen; whatever unused rows hold (NaN scales, any exponent) stays out."""
     c, q, table, kv, cu = _problem(ba, qn, [210, 170], 4, 2, 128, 48, "bf16", 4)
@@ -333,7 +333,7 @@ def test_missing_pages_and_garbage_outside_the_sequences(ba, qn, causal):
     _compare(*_run(ba, prob, causal=causal), _ref(ba, prob, causal=causal))
 
 
-@pytest.mark.parametrize("qn", [[2, 3], [40, 30]])
+@pytest.mark.parametrize("qn", [[2, 3], [40, 30], [70, 80]])
 def test_rows_of_no_sequence_stay(ba, qn):
     """Rows behind the last sequence, before the first and past max_q_len are left as they were."""
     c, q, table, kv, cu = _problem(ba, qn, [50, 90], 4, 2, 64, 16, "bf16", 6)
@@ -346,6 +346,8 @@ def test_rows_of_no_sequence_stay(ba, qn):
     assert got is out
     assert (out[:2] == 5).all() and (out[2 + sum(qn):] == 5).all() and torch.equal(out[2:2 + sum(qn)], want)
     out.fill_(5.0)
+    # another bound may choose another kernel, whose roundings are others
+    want = _run(ba, (c, q, table, kv, cu), max_q_len=qn[0])[0]
     ba.attention_paged(q2.cuda(), c, table.cuda(), kv.cuda(), cu2.cuda(), max_q_len=qn[0], out=out)
     n = min(qn)
     assert torch.equal(out[2:2 + n], want[:n])
@@ -380,6 +382,66 @@ def test_split_key_axis(ba, kn, Hq, Hkv, d):
     _compare(*_run(ba, prob, max_q_len=1), _ref(ba, prob))
     kw = dict(window=5000, sinks=70)
     _compare(*_run(ba, prob, max_q_len=1, **kw), _ref(ba, prob, **kw))
+
+
+@pytest.mark.parametrize("qn,kn,Hq,Hkv,d,ps,dt", [([40], [3001], 4, 1, 128, 64, "bf16"),
+                                                  ([20, 70], [2500, 400], 8, 2, 64, 32, "f16")])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1500, 200)])
+def test_chunks_split_over_the_key_axis(ba, qn, kn, Hq, Hkv, d, ps, dt, window, sinks):
+    """Few chunks over long contexts: the key blocks of one tile are cut over many CTAs and joined."""
+    prob = _problem(ba, qn, kn, Hq, Hkv, d, ps, dt, 30)
+    kw = dict(window=window, sinks=sinks)
+    _compare(*_run(ba, prob, max_q_len=max(qn), **kw), _ref(ba, prob, **kw))
+
+
+@pytest.mark.parametrize("qn,Hq,Hkv,d", [([3, 2], 8, 2, 128), ([4], 8, 2, 64), ([5, 1, 6], 5, 1, 100), ([8, 8], 2, 1, 33),
+                                         ([25, 9], 4, 2, 128), ([60, 100], 1, 1, 80)])
+@pytest.mark.parametrize("n", [200, 5000])
+def test_several_tiles_of_sixteen_rows(ba, qn, Hq, Hkv, d, n):
+    prob = _problem(ba, qn, [n - 7 * b for b in range(len(qn))], Hq, Hkv, d, 32, "bf16", 31 + d)
+    kw = dict(max_q_len=max(qn))
+    _compare(*_run(ba, prob, **kw), _ref(ba, prob, **kw))
+
+
+@pytest.mark.parametrize("qn", [[1], [20], [70]])
+def test_windows_and_sinks_of_any_size(ba, qn):
+    """A window or sinks beyond every position hide nothing, also where a sequence starts before its first key."""
+    prob = _problem(ba, qn, [33], 4, 2, 64, 16, "bf16", 32)
+    want = _run(ba, prob)
+    for window, sinks in (((1 << 31) - 1, 0), ((1 << 31) - 1, (1 << 31) - 1), (1 << 40, 3), (1, 1 << 33), (1 << 28, 0)):
+        got = _run(ba, prob, window=window, sinks=sinks, max_q_len=1 << 35, max_kv_len=1 << 40)
+        _compare(*got, _ref(ba, prob))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("qn", [[1], [40], [80]])
+def test_garbage_on_pages_before_the_window(ba, qn):
+    """A table may go on naming pages that the window has left behind: their next use does not show."""
+    ps, n, window, sinks = 16, 300, 50, 4
+    c, q, table, kv, cu = _problem(ba, qn, [n], 4, 2, 128, ps, "bf16", 33)
+    first = (n - qn[0] - window + 1) // ps
+    for j in range(1, first):
+        c.data[int(table[0, j])] = 0x80  # codes of -128, negative scales
+        c.v_exp[int(table[0, j])] = 127
+    prob = (c, q, table, kv, cu)
+    kw = dict(window=window, sinks=sinks)
+    _compare(*_run(ba, prob, **kw), _ref(ba, prob, **kw))
+
+
+@pytest.mark.parametrize("qn", [[1], [40], [80]])
+def test_negative_scales_behind_a_sequence_that_ends_in_its_largest_keys(ba, qn):
+    """The last, partly filled block has scores far above all before: what lies behind it must not hide that."""
+    d, ps, n = 128, 64, 128 * 3 + 10
+    g = _gen(34)
+    c = ba.KVCache.zeros(8, 1, d, ps)
+    c.data.fill_(0xC0)
+    k, v = (torch.randn((n, 1, d), generator=g).bfloat16() for _ in range(2))
+    q = torch.randn((qn[0], 2, d), generator=g).bfloat16()
+    k[-10:] = q[-1, 0] * 30
+    ba.cache_write(c, k.cuda(), v.cuda(), torch.arange(n).cuda())
+    prob = (c, q, torch.arange(8, dtype=torch.int32)[None], torch.tensor([n], dtype=torch.int32), torch.tensor([0] + qn, dtype=torch.int32))
+    for causal in (True, False):
+        _compare(*_run(ba, prob, causal=causal), _ref(ba, prob, causal=causal))
 
 
 def test_results_repeat_bit_for_bit(ba):
@@ -537,7 +599,8 @@ def test_binding_refusals(ba):
         ba.cache_read(c, ok, torch.int8)
     for kw in (dict(q=q.float()), dict(q=q[..., :32]), dict(q=q.cpu()), dict(page_table=table.long()),
                dict(page_table=table[:1]), dict(kv_lens=kv.long()), dict(cu_seqlens_q=cu[:2]), dict(cu_seqlens_q=cu.cpu()),
-               dict(out=q[:1]), dict(out=q.float(), out_dtype=torch.bfloat16)):
+               dict(out=q[:1]), dict(out=q.float(), out_dtype=torch.bfloat16), dict(workspace=torch.zeros(64, dtype=torch.uint8)),
+               dict(workspace=torch.zeros((1 << 20, 2), dtype=torch.uint8, device="cuda")[:, 0])):
         args = dict(q=q, page_table=table, kv_lens=kv, cu_seqlens_q=cu)
         args.update(kw)
         with pytest.raises(ValueError):
