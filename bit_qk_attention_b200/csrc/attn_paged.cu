@@ -124,7 +124,7 @@ __device__ __forceinline__ float2 whole(int x, int y) {
 
 // Shared memory of a warp: V rows of kRow bytes for each stage as the tensor map's swizzle leaves
 // them, then each stage's sign rows, mu and exponents. Once a block's sign rows are read, what its
-// scores need per key as floats (mu, e, 2^-e) takes their place. Three CTAs of four warps just fit an SM.
+// scores need per key as floats (mu, e, 2^-e) takes their place. Three CTAs of four warps just fit an SM
 template <int CPG>  // eighths of the channels: 16 (rows of 128 bytes) or 8 (rows of 64)
 struct Ring {
   static constexpr int kRow = CPG * 8;
@@ -171,15 +171,19 @@ __device__ __forceinline__ float lds_cluster(uint32_t a, int rank) {
   return x;
 }
 
-// NR = 2 needs 255 registers, so that two CTAs fit an SM: with three, and 230 bytes of spills, 16 rows of
-// 32 x 4096 keys and 8 KV heads (d = 128) took 70 us instead of 49.
+// CTAs on an SM. Two tiles of 8 rows need 255 registers: with three CTAs, and 230 bytes of spills, 16 rows
+// of 32 x 4096 keys and 8 KV heads (d = 128) took 70 us instead of 49. Up to 64 channels fit 128 registers:
+// 16 heads of 32 x 4096 keys in a window (d = 64) take 41 us with four, 46 with three, 43 with five and spills.
+constexpr int ctas_per_sm(int cpg, int nr) { return nr == 2 ? 2 : (cpg == 16 ? 3 : 4); }
+
 template <int CPG, int NR>
-__global__ void __launch_bounds__(kThreads, NR == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(CPG, NR))
     paged_decode_kernel(PagedAttnParams p, int q_f16, int unit, const __grid_constant__ CUtensorMap v_map) {
   using S = Ring<CPG>;
   constexpr int MT = CPG / 2;  // 16-channel tiles
   constexpr int R = 8 * NR;    // rows of a CTA
   constexpr int CH = CPG * 8;  // channels of the accumulators (>= d)
+  constexpr int KS = CPG / 2;  // steps of QK, four channels of each thread
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int oBits = S::offBits(R), oMu = S::offMu(R), oScratch = S::offScratch(R);
   auto s_full = reinterpret_cast<uint64_t(*)[kStages]>(smem + S::offFull);
@@ -336,18 +340,20 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 3 : 2)
   __syncthreads();
 
   // Q as the B operand, row g: this thread's bytes meet word t of the keys; byte i of step s is
-  // channel 32 t + 8 i + s, and holds +-2^(6 - s) (s = 7: +-1, its bit is moved down by one).
-  uint32_t qb[NR][8];
+  // channel 32 t + 8 i + s, and holds +-2^(6 - s) (s = 7: +-1, its bit is moved down by one). Up to 64
+  // channels: word t % 2, of each of its bytes the upper half if t > 1.
+  const int tw = CPG == 16 ? t : t & 1, sh = CPG == 16 ? 0 : 4 * (t >> 1);
+  uint32_t qb[NR][KS];
   // Of the rows 2 t and 2 t + 1, which this thread's scores belong to:
   float2 cq[NR], back[NR];
   int last[NR][2], wlo[NR][2];  // the row sees keys j <= last with j >= wlo or j < sinks
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
-    const uint32_t word = s_bits[8 * n + g][t];
-    const int nc = cv.d - 32 * t;  // channels of this word
-    const uint32_t live = nc >= 32 ? 0xffffffffu : (nc <= 0 ? 0u : (1u << nc) - 1u);
+    const uint32_t word = s_bits[8 * n + g][tw] >> sh;
+    const int nc = cv.d - 32 * tw;  // channels of this word
+    const uint32_t live = (nc >= 32 ? 0xffffffffu : (nc <= 0 ? 0u : (1u << nc) - 1u)) >> sh;
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
+    for (int s = 0; s < KS; ++s) {
       // Bytes mag, or 256 - mag where the bit is set; 0 where there is no channel.
       const uint32_t mag = 1u << (s == 7 ? 0 : 6 - s);
       qb[n][s] = (0x01010101u * mag + ((word >> s) & 0x01010101u) * (256u - 2u * mag)) &
@@ -405,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 3 : 2)
 #pragma unroll
     for (int h = 0; h < kQ; ++h)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) word[h][k] = lds32(fl + (16 * h + key0 + 2 * k) * 16 + 4 * t);
+      for (int k = 0; k < 2; ++k) word[h][k] = lds32(fl + (16 * h + key0 + 2 * k) * 16 + 4 * tw) >> sh;
     {
       uint32_t mu[kBlk / 32];
       int e[kBlk / 32];
@@ -428,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 3 : 2)
     for (int h = 0; h < kQ; ++h) {
       int x[NR][4];  // 64 sum q k of 16 keys and 8 rows
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
+      for (int s = 0; s < KS / 2; ++s) {
         const uint32_t a0 = word[h][0] & (0x01010101u << (2 * s)), a1 = word[h][1] & (0x01010101u << (2 * s));
         const uint32_t a2 = s == 3 ? (word[h][0] >> 1) & 0x40404040u : word[h][0] & (0x02020202u << (2 * s));
         const uint32_t a3 = s == 3 ? (word[h][1] >> 1) & 0x40404040u : word[h][1] & (0x02020202u << (2 * s));
@@ -770,7 +776,7 @@ cudaError_t launch_paged_decode(const PagedAttnParams& p, int dt, cudaStream_t s
 void paged_decode_plan(PagedAttnParams* p, int sms) {
   const int64_t blocks = std::max<int64_t>(1, most_blocks(*p, p->row_tile, kBlk));
   const int64_t tiles = static_cast<int64_t>(p->B) * p->row_tiles * p->cache.heads;
-  const int64_t fit = static_cast<int64_t>(sms) * (p->row_tile > 8 ? 2 : 3);  // CTAs at once, by registers
+  const int64_t fit = static_cast<int64_t>(sms) * ctas_per_sm(p->cache.dp > 64 ? 16 : 8, p->row_tile / 8);  // CTAs at once
   // Short contexts: a cluster of up to eight CTAs per (tile, head), down to a block per warp, joins
   // its parts itself. Where that leaves a warp more than kShort blocks beyond its share of an even
   // split over the GPU (or more than kShort of them, when the CTAs do not fit at once and ragged
