@@ -70,13 +70,13 @@ struct Cfg {
   static constexpr int offExp = offMu + kBlk * 2;
   static constexpr int offBar = offExp + kBlk;
   static constexpr int kToken = kRow + 16 + 2 + 1;  // bytes that a token brings
-  static constexpr int kNumBars = 24;
+  static constexpr int kNumBars = 26;
   static constexpr int offMisc = offBar + kNumBars * 8;  // tensor memory base, abort flag, page masks [4]
   static constexpr int offTop = offMisc + 8 + 16;  // [block % 4][expanding warp]: largest mu of its keys
   static constexpr int offScratch = offTop + 64;
   static constexpr int kBytes = offScratch + (kThreads / 32 + 2) * 8;
   static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
-  // Tensor memory: S of tile q (P over its second half), then O.
+  // Tensor memory: S of tile q in two halves of 64 keys, each with its P over it, then O.
   static __host__ __device__ constexpr uint32_t tS(int q) { return q * 128; }
   static __host__ __device__ constexpr uint32_t tO(int q) { return 256 + q * CH; }
   // Byte offset of the 16-byte piece c of key j's V row: the swizzle of 128- or 64-byte rows.
@@ -85,9 +85,10 @@ struct Cfg {
   }
 };
 
-// Barriers. K and V operands: per stage. The others: per tile; S by halves of the keys.
-constexpr int bKfull = 0, bKempty = 2, bVfull = 4, bVempty = 6, bQfull = 8, bS = 10, bRead = 14, bP = 16, bPV = 18,
-              bDrain = 20, bRawFull = 22, bRawEmpty = 23;
+// Barriers. K and V operands: per stage. The others: per tile; S, P and P V by halves of the keys, since
+// who waits for the last P V may not have seen the one before.
+constexpr int bKfull = 0, bKempty = 2, bVfull = 4, bVempty = 6, bQfull = 8, bS = 10, bP = 14, bPV = 18, bDrain = 22,
+              bRawFull = 24, bRawEmpty = 25;
 
 // The (tile, head)s of a CTA one after the other, as every role walks them.
 struct Walk {
@@ -232,10 +233,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
       mbar_init(&bars[bVempty + i], 2);
       mbar_init(&bars[bDrain + i], 1);
       mbar_init(&bars[bQfull + i], 4);
-      mbar_init(&bars[bRead + i], 4);
-      mbar_init(&bars[bPV + i], 1);
-      mbar_init(&bars[bP + i], 4);
-      for (int h = 0; h < 2; ++h) mbar_init(&bars[bS + 2 * i + h], 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&bars[bS + 2 * i + h], 1);
+        mbar_init(&bars[bP + 2 * i + h], 4);
+        mbar_init(&bars[bPV + 2 * i + h], 1);
+      }
     }
     mbar_init(&bars[bRawFull], 1);
     mbar_init(&bars[bRawEmpty], 4);
@@ -281,11 +283,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
             mma_f16_ss(s_t + 64 * h, k_desc | (q_at + i * 256), k_desc | (ka + i * 256), id_qk, i > 0 ? 1u : 0u);
         tc_commit(&bars[bS + 2 * q + h]);
       };
-      auto pv = [&](int st, uint32_t more) {
-        const uint32_t va = v_at + st * (C::kOp / 16);
+      // P V of those keys.
+      auto pv = [&](int st, int h, uint32_t more) {
+        const uint32_t va = v_at + st * (C::kOp / 16) + h * 64;
 #pragma unroll
-        for (int i = 0; i < kBlk / 16; ++i)
-          mma_f16_ts(o_t, s_t + 64 + 8 * i, v_desc | (va + 16 * i), id_pv, i > 0 ? 1u : more);
+        for (int i = 0; i < kBlk / 32; ++i)
+          mma_f16_ts(o_t, s_t + 64 * h + 8 * i, v_desc | (va + 16 * i), id_pv, i > 0 ? 1u : more);
+        tc_commit(&bars[bPV + 2 * q + h]);
       };
       int g = 0, c = 0, seg = 0;  // blocks of the CTA, blocks and (tile, head)s of this tile so far
       bool ok = true;
@@ -308,19 +312,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
         tc_commit(&bars[bKempty + (g & 1)]);
         for (int n = 0; n < k.n_blk && ok; ++n, ++g, ++c) {
           const bool more = n + 1 < k.n_blk;
-          if (more) {
-            if (!wait(bRead + q, c) || !wait(bKfull + ((g + 1) & 1), (g + 1) >> 1)) break;
+#pragma unroll
+          for (int h = 0; h < 2 && ok; ++h) {
+            if (!wait(bP + 2 * q + h, c) || (h == 0 && !wait(bVfull + (g & 1), g >> 1))) break;
             tc_fence_after();
-            qk((g + 1) & 1, 0);
-          }
-          if (!wait(bP + q, c) || !wait(bVfull + (g & 1), g >> 1)) break;
-          tc_fence_after();
-          pv(g & 1, n > 0 ? 1u : 0u);
-          tc_commit(&bars[bPV + q]);
-          tc_commit(&bars[bVempty + (g & 1)]);
-          if (more) {
-            qk((g + 1) & 1, 1);  // over P, after P V
-            tc_commit(&bars[bKempty + ((g + 1) & 1)]);
+            pv(g & 1, h, n > 0 || h > 0 ? 1u : 0u);
+            if (h == 1) tc_commit(&bars[bVempty + (g & 1)]);
+            if (more) {  // the next block's scores take the place of these weights, after P V
+              if (h == 0 && !wait(bKfull + ((g + 1) & 1), (g + 1) >> 1)) break;
+              tc_fence_after();
+              qk((g + 1) & 1, h);
+              if (h == 1) tc_commit(&bars[bKempty + ((g + 1) & 1)]);
+            }
           }
         }
         ++seg;
@@ -482,14 +485,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
       const int all_lo = __reduce_max_sync(0xffffffffu, live ? wlo : -0x7fffffff);
       float M = -CUDART_INF_F, l = 0.0f;
       if (!mine) g += n_blk;
-      // A score passes M by more than the slack: M moves, and what there is of the row is rescaled by
-      // the factor that comes back. O holds the blocks before n.
-      auto move_to = [&](float top, int n) {
+      // A score passes M by more than the slack: M moves, and what there is of the row is rescaled. O
+      // holds the halves before half h of block n.
+      auto move_to = [&](float top, int n, int h) {
         const bool moves = top > M + kSlack;
         const float f = moves ? ex2_approx(M - top) : 1.0f;  // 0 for a row's first keys
         if (moves) M = top;
         l *= f;
-        if (n > 0 && (ok = wait_warp<false>(&bars[bPV + q], (c - 1) & 1, abort_flag))) {
+        if (n + h > 0 && (ok = wait_warp<false>(&bars[bPV + 2 * q + 1 - h], (c - 1 + h) & 1, abort_flag))) {
           tc_fence_after();
 #pragma unroll 1
           for (int i = 0; i < cv.dp; i += 16) {
@@ -503,25 +506,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
             tmem_st16p(aO + i, o);
           }
         }
-        return f;
       };
       auto arrive = [&](int bar) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[bar]);
       };
-      auto read = [&](int at, uint32_t (&s)[32]) { tmem_ld32p(aS + at, s); };
       auto arrived = [&](uint32_t (&s)[32]) {
         tmem_ld_wait();
         reg_fence32(s);
       };
-      // Which of the keys j .. j + 31 the row sees.
-      auto seen = [&](int j, uint32_t pages) {
-        return low_bits(last - j + 1) & (~low_bits(wlo - j) | low_bits(p.sinks - j)) &
-               ((pages & 1u) * 0xffffu | (pages >> 1 & 1u) * 0xffff0000u);
-      };
-      auto mask = [&](uint32_t (&s)[32], uint32_t see) {
-        __syncwarp();  // keeps the callers' conditions branches
+      // Scores of the keys j .. j + 31 that the row does not see (`pages`: which 16 of them have a page).
+      auto mask = [&](uint32_t (&s)[32], int j, uint32_t pages) {
+        const uint32_t see = low_bits(last - j + 1) & (~low_bits(wlo - j) | low_bits(p.sinks - j)) &
+                             ((pages & 1u) * 0xffffu | (pages >> 1 & 1u) * 0xffff0000u);
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           if (!((see >> i) & 1u)) s[i] = 0xff800000u;  // -inf
@@ -540,101 +538,65 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
       };
       for (int n = 0; n < n_blk && mine && ok; ++n, ++g, ++c) {
         const int j0 = w.block_at(v0 + n) * kBlk;
-        if (!(ok = wait_warp<false>(&bars[bS + 2 * q], c & 1, abort_flag))) break;
-        tc_fence_after();
-        const uint32_t have = page_ok[g & 3];
-        // Quarters (32 keys) from here on are read twice.
-        int again = have == 0xffu && j0 + kBlk - 1 <= all_last && j0 >= all_lo &&
-                    !__any_sync(0xffffffffu, live && M == -CUDART_INF_F) ? 4 : 0;
-        uint32_t pw[2][32];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h == 1) {
-            if (!(ok = wait_warp<false>(&bars[bS + 2 * q + 1], c & 1, abort_flag))) break;
-            tc_fence_after();
-          }
-          if (again == 4) {
-            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-            uint32_t x[32], y[32];
-            read(64 * h, x);
-            arrived(x);
-            read(64 * h + 32, y);
-            weigh(x, pw[h], M, sum);
-            arrived(y);
-            weigh(y, pw[h] + 16, M, sum);
-            const float all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            if (__all_sync(0xffffffffu, !live || all <= kMostSum)) {
-              l += all;
-              if (h == 0) arrive(bRead + q);
-            } else {
-              again = 2 * h;
-            }
-          }
-        }
-        if (!ok) break;
-        if (again < 4) {
-          float top = -CUDART_INF_F;
-          uint32_t x[32];
-          // A mask alone needs no maximum where none can pass M by 2^15: |score| <= factor * d * mu.
-          const volatile float* most = reinterpret_cast<volatile float*>(smem + C::offTop + (g & 3) * 16);
-          const float mu_top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-          const bool known = __all_sync(0xffffffffu, !live || cq * static_cast<float>(cv.d) * mu_top <= M + kMostLog2);
-          // Which of its 32 keys the row sees.
-          auto seen = [&](int quarter) {
-            const int j = j0 + 32 * quarter;
-            const uint32_t pages = have >> (2 * quarter);
-            return low_bits(last - j + 1) & (~low_bits(wlo - j) | low_bits(p.sinks - j)) &
-                   ((pages & 1u) * 0xffffu | (pages >> 1 & 1u) * 0xffff0000u);
-          };
 #pragma unroll 1
-          for (int k = known ? 4 : again; k < 4; ++k) {
-            read(32 * k, x);
-            const uint32_t see = seen(k);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t at = aS + 64 * h;
+          const int j = j0 + 64 * h;
+          if (!(ok = wait_warp<false>(&bars[bS + 2 * q + h], c & 1, abort_flag))) break;
+          tc_fence_after();
+          const uint32_t have = page_ok[g & 3] >> (4 * h) & 15u;
+          uint32_t x[32], y[32], pw[32];
+          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+          float all = 0.0f;
+          bool done = have == 15u && j + 63 <= all_last && j >= all_lo && !__any_sync(0xffffffffu, live && M == -CUDART_INF_F);
+          if (done) {
+            tmem_ld32p(at, x);
             arrived(x);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) top = fmaxf(top, (see >> i) & 1u ? __uint_as_float(x[i]) : -CUDART_INF_F);
+            tmem_ld32p(at + 32, y);
+            weigh(x, pw, M, sum);
+            arrived(y);
+            weigh(y, pw + 16, M, sum);
+            all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            done = __all_sync(0xffffffffu, !live || all <= kMostSum);
           }
-          top *= cq;
-          if (!known && __any_sync(0xffffffffu, top > M + kSlack)) {
-            const float f = move_to(top, n);
-            if (!ok) break;
-            if (again == 2) {  // the first half's weights, already fp16, are rounded once more
-              const __half2 f2 = __float2half2_rn(f);
+          if (!done) {
+            tmem_ld32p(at, x);
+            tmem_ld32p(at + 32, y);
+            arrived(x);
+            reg_fence32(y);
+            mask(x, j, have);
+            mask(y, j + 32, have >> 2);
+            // A mask alone needs no maximum where none can pass M by 2^15: |score| <= factor * d * mu.
+            const volatile float* most = reinterpret_cast<volatile float*>(smem + C::offTop + (g & 3) * 16 + h * 8);
+            const float mu_top = fmaxf(most[0], most[1]);
+            if (!__all_sync(0xffffffffu, !live || cq * static_cast<float>(cv.d) * mu_top <= M + kMostLog2)) {
+              float top = -CUDART_INF_F;
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&pw[0][i]), f2);
-                pw[0][i] = *reinterpret_cast<const uint32_t*>(&y);
+              for (int i = 0; i < 32; ++i) top = fmax3(top, __uint_as_float(x[i]), __uint_as_float(y[i]));
+              top *= cq;
+              if (__any_sync(0xffffffffu, top > M + kSlack)) {
+                move_to(top, n, h);
+                if (!ok) break;
               }
             }
+            sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+            const float ref = M == -CUDART_INF_F ? 0.0f : M;
+            weigh(x, pw, ref, sum);
+            weigh(y, pw + 16, ref, sum);
+            all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           }
-          // From the last quarter down: P of a quarter lies over scores that have been read.
-          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll 1
-          for (int k = 3; k >= again; --k) {
-            read(32 * k, x);
-            const uint32_t see = seen(k);
-            arrived(x);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((see >> i) & 1u)) x[i] = 0xff800000u;  // -inf
-            uint32_t y[16];
-            weigh(x, y, M == -CUDART_INF_F ? 0.0f : M, sum);
-            tmem_st16p(aS + 64 + 16 * k, y);
-          }
-          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-          if (again == 0) arrive(bRead + q);
+          l += all;
+          tmem_st32p(at, pw);
+          tmem_st_wait();
+          arrive(bP + 2 * q + h);
         }
-        if (again > 0) tmem_st32p(aS + 64, pw[0]);
-        if (again == 4) tmem_st32p(aS + 96, pw[1]);
-        tmem_st_wait();
-        arrive(bP + q);
       }
       if (!ok) break;
       // The next (tile, head)'s scores can be made while this one's rows are written.
       if (write_next) cq_next = write_q(k);
       if (!mine) continue;
       // ------------------------------------------------------------ the rows' results
-      if (n_blk > 0 && !(ok = wait_warp<false>(&bars[bPV + q], (c - 1) & 1, abort_flag))) break;
+      if (n_blk > 0 && !(ok = wait_warp<false>(&bars[bPV + 2 * q + 1], (c - 1) & 1, abort_flag))) break;
       tc_fence_after();
       const int64_t out = out_row(p, w, head, r);
       const float inv = slot >= 0 ? 1.0f : (l > 0.0f ? 1.0f / l : 0.0f);
