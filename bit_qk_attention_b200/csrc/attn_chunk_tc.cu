@@ -59,16 +59,18 @@ constexpr uint64_t kTimeoutNs = 1000000000ull;
 
 template <int CH>  // channels of the operands: 64 or 128 (>= d)
 struct Cfg {
-  static constexpr int kOp = kBlk * CH * 2;  // bytes of an operand tile of 128 rows
+  static constexpr int kOp8 = kBlk * CH;      // bytes of an operand tile of 128 rows: Q and K
+  static constexpr int kOp16 = kBlk * CH * 2;  // and V
   static constexpr int kRow = CH;            // bytes of a V row in the stage
   static constexpr int offQ = 0;
-  static constexpr int offK = offQ + 2 * kOp;
-  static constexpr int offV = offK + 2 * kOp;
-  static constexpr int offRaw = offV + 2 * kOp;  // the cache rows of a block: codes, sign rows, mu, exponents
+  static constexpr int offK = offQ + 2 * kOp8;
+  static constexpr int offV = offK + 2 * kOp8;
+  static constexpr int offRaw = offV + 2 * kOp16;  // the cache rows of a block: codes, sign rows, mu, exponents
   static constexpr int offBits = offRaw + kBlk * kRow;
   static constexpr int offMu = offBits + kBlk * 16;
   static constexpr int offExp = offMu + kBlk * 2;
-  static constexpr int offBar = offExp + kBlk;
+  static constexpr int offScale = offExp + kBlk;  // [block % 4][key]: mu as floats
+  static constexpr int offBar = offScale + 4 * kBlk * 4;
   static constexpr int kToken = kRow + 16 + 2 + 1;  // bytes that a token brings
   static constexpr int kNumBars = 26;
   static constexpr int offMisc = offBar + kNumBars * 8;  // tensor memory base, abort flag, page masks [4]
@@ -154,19 +156,17 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
 // The n lowest bits (none below 0, all from 32 on).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
 
-// Sign bits of 32 channels -> 16 pairs (channel p, channel p + 16) of +-m, m the bf16 pair (mu, mu):
-// four 16-byte pieces of a K-major operand row. keep[i] masks channels that do not exist.
-__device__ __forceinline__ void expand_signs(uint32_t dst, uint32_t word, uint32_t m, uint32_t live) {
+// Sign bits of 32 channels -> +-1 in e4m3, two 16-byte pieces of a K-major operand row. Byte b of word i
+// is channel 8 b + i, so that one shift and one mask place four signs; Q and K have the same order, and
+// a dot product does not mind. `live`: channels that exist, the others are 0.
+__device__ __forceinline__ void expand_signs(uint32_t dst, uint32_t word, uint32_t live) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < 2; ++c) {
     uint32_t x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int p = 4 * c + i;
-      const uint32_t mm = live == 0xffffffffu
-                              ? m
-                              : ((live >> p) & 1u ? m & 0xffffu : 0u) | ((live >> (p + 16)) & 1u ? m & 0xffff0000u : 0u);
-      x[i] = ((word << (15 - p)) & 0x80008000u) ^ mm;
+      x[i] = ((word << (7 - 4 * c - i)) & 0x80808080u) ^ 0x38383838u;
+      if (live != 0xffffffffu) x[i] &= ((live >> (4 * c + i)) & 0x01010101u) * 255u;
     }
     sts128(dst + c * 2048, x[0], x[1], x[2], x[3]);
   }
@@ -267,25 +267,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
     if (warp < 2 && lane == 0) {
       // ---------------------------------------------------------- MMA issue of tile `warp`
       const int q = warp;
-      const uint32_t id_qk = (1u << 4) | (1u << 7) | (1u << 10) | ((kBlk / 2 >> 3) << 17) | ((kTile >> 4) << 24);
+      const uint32_t id_qk = (1u << 4) | ((kBlk / 2 >> 3) << 17) | ((kTile >> 4) << 24);
       const uint32_t id_pv = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(cv.dp >> 3) << 17) | ((kTile >> 4) << 24);
-      const int qk_steps = 2 * ((cv.d + 31) / 32);
+      const int qk_steps = (cv.d + 31) / 32;
       const uint32_t s_t = tmem + C::tS(q), o_t = tmem + C::tO(q);
       // Descriptors: the address part (in units of 16 bytes) of the first step, and what is fixed.
       const uint64_t k_desc = smem_desc(0, 2048, 128), v_desc = smem_desc(0, 128, 2048);
-      const uint32_t q_at = (base + C::offQ + q * C::kOp) >> 4, k_at = (base + C::offK) >> 4, v_at = (base + C::offV) >> 4;
+      const uint32_t q_at = (base + C::offQ + q * C::kOp8) >> 4, k_at = (base + C::offK) >> 4, v_at = (base + C::offV) >> 4;
       // Scores of the keys 64 h .. 64 h + 63 of the block in stage st.
       auto qk = [&](int st, int h) {
-        const uint32_t ka = k_at + st * (C::kOp / 16) + h * 64;
+        const uint32_t ka = k_at + st * (C::kOp8 / 16) + h * 64;
 #pragma unroll
-        for (int i = 0; i < CH / 16; ++i)
+        for (int i = 0; i < CH / 32; ++i)
           if (i < qk_steps)
-            mma_f16_ss(s_t + 64 * h, k_desc | (q_at + i * 256), k_desc | (ka + i * 256), id_qk, i > 0 ? 1u : 0u);
+            mma_f8_ss(s_t + 64 * h, k_desc | (q_at + i * 256), k_desc | (ka + i * 256), id_qk, i > 0 ? 1u : 0u);
         tc_commit(&bars[bS + 2 * q + h]);
       };
       // P V of those keys.
       auto pv = [&](int st, int h, uint32_t more) {
-        const uint32_t va = v_at + st * (C::kOp / 16) + h * 64;
+        const uint32_t va = v_at + st * (C::kOp16 / 16) + h * 64;
 #pragma unroll
         for (int i = 0; i < kBlk / 32; ++i)
           mma_f16_ts(o_t, s_t + 64 * h + 8 * i, v_desc | (va + 16 * i), id_pv, i > 0 ? 1u : more);
@@ -399,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
         // A row behind the sequence may hold a negative mu: its sign would hide the others.
         const uint32_t mu_top = __reduce_max_sync(0xffffffffu, mu & 0x7fffu);
         if (lane == 0) *reinterpret_cast<volatile float*>(smem + C::offTop + (g & 3) * 16 + (warp - 4) * 4) = __uint_as_float(mu_top << 16);
+        *reinterpret_cast<volatile float*>(smem + C::offScale + ((g & 3) * kBlk + row) * 4) = __uint_as_float(mu << 16);
         uint4 code[CH / 16];
 #pragma unroll
         for (int c = 0; c < CH / 16; ++c)
@@ -406,16 +407,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[bRawEmpty]);
         if (g >= 2 && !(ok = wait_warp<true>(&bars[bKempty + st], ((g >> 1) - 1) & 1, abort_flag))) break;
-        const uint32_t kd = base + C::offK + st * C::kOp + row * 16;
+        const uint32_t kd = base + C::offK + st * C::kOp8 + row * 16;
         const uint32_t word[4] = {bits.x, bits.y, bits.z, bits.w};
 #pragma unroll
         for (int i = 0; i < CH / 32; ++i)
-          if (32 * i < cv.d) expand_signs(kd + i * 8192, word[i], mu | (mu << 16), 0xffffffffu);
+          if (32 * i < cv.d) expand_signs(kd + i * 4096, word[i], 0xffffffffu);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[bKfull + st]);
         if (g >= 2 && !(ok = wait_warp<true>(&bars[bVempty + st], ((g >> 1) - 1) & 1, abort_flag))) break;
-        const uint32_t vd = base + C::offV + st * C::kOp + row * 16;
+        const uint32_t vd = base + C::offV + st * C::kOp16 + row * 16;
         // A row that no query row sees may hold anything: times 0 it is finite, as its weight of 0 needs.
         const int j = k.w.block_at(k.v0 + n) * kBlk + row;
         const bool in = j < k.w.kv && (j >= k.w.lo || j < p.sinks);
@@ -451,11 +452,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
         mu = p.q_mu[at];
       }
       const uint32_t w4x[4] = {word.x, word.y, word.z, word.w};
-      const uint32_t qd = base + C::offQ + q * C::kOp + (w4 * 32 + lane) * 16;
+      const uint32_t qd = base + C::offQ + q * C::kOp8 + (w4 * 32 + lane) * 16;
 #pragma unroll
       for (int i = 0; i < CH / 32; ++i) {
         const int n = cv.d - 32 * i;
-        if (n > 0) expand_signs(qd + i * 8192, w4x[i], 0x3f803f80u, low_bits(n));
+        if (n > 0) expand_signs(qd + i * 4096, w4x[i], low_bits(n));
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -516,24 +517,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
         tmem_ld_wait();
         reg_fence32(s);
       };
-      // Scores of the keys j .. j + 31 that the row does not see (`pages`: which 16 of them have a page).
-      auto mask = [&](uint32_t (&s)[32], int j, uint32_t pages) {
-        const uint32_t see = low_bits(last - j + 1) & (~low_bits(wlo - j) | low_bits(p.sinks - j)) &
-                             ((pages & 1u) * 0xffffu | (pages >> 1 & 1u) * 0xffff0000u);
+      // Sixteen scores of the keys from j on, -inf for those that the row does not see.
+      auto read16 = [&](uint32_t from, int j, bool page, uint32_t mu, uint32_t (&s)[16]) {
+        tmem_ld16p(from, s);
+        const uint32_t see = page ? low_bits(last - j + 1) & (~low_bits(wlo - j) | low_bits(p.sinks - j)) : 0u;
+        tmem_ld_wait();
+        reg_fence8(s);
+        reg_fence8(s + 8);
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (!((see >> i) & 1u)) s[i] = 0xff800000u;  // -inf
+        for (int i = 0; i < 4; ++i) {
+          const uint4 m = lds128(mu + 16 * i);
+          const uint32_t m4[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+          for (int e = 4 * i; e < 4 * i + 4; ++e)
+            s[e] = (see >> e) & 1u ? __float_as_uint(__uint_as_float(s[e]) * __uint_as_float(m4[e % 4])) : 0xff800000u;
+        }
       };
-      // Weights of 32 keys as 16 fp16 pairs; their sums are added to `sum`.
-      auto weigh = [&](const uint32_t (&s)[32], uint32_t* to, float ref, float2 (&sum)[2]) {
-        const float2 c2 = make_float2(cq, cq), m2 = make_float2(-ref, -ref);
+      // The weight of two keys as an fp16 pair; its numbers are added to `sum`.
+      auto weigh = [&](float2 x, float ref, float2& sum) {
+        x = __ffma2_rn(x, make_float2(cq, cq), make_float2(-ref, -ref));
+        const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+        sum = __fadd2_rn(sum, e);
+        const __half2 y = __floats2half2_rn(e.x, e.y);
+        return *reinterpret_cast<const uint32_t*>(&y);
+      };
+      // Of 32 keys with the scales at `mu`.
+      auto weigh32 = [&](const uint32_t (&s)[32], uint32_t mu, uint32_t* to, float2 (&sum)[2]) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, m2);
-          const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-          sum[i & 1] = __fadd2_rn(sum[i & 1], e);
-          const __half2 y = __floats2half2_rn(e.x, e.y);
-          to[i] = *reinterpret_cast<const uint32_t*>(&y);
+        for (int i = 0; i < 8; ++i) {
+          const uint4 m = lds128(mu + 16 * i);
+          const float2 a = __fmul2_rn(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])),
+                                      make_float2(__uint_as_float(m.x), __uint_as_float(m.y)));
+          const float2 b = __fmul2_rn(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])),
+                                      make_float2(__uint_as_float(m.z), __uint_as_float(m.w)));
+          to[2 * i] = weigh(a, M, sum[0]);
+          to[2 * i + 1] = weigh(b, M, sum[1]);
         }
       };
       for (int n = 0; n < n_blk && mine && ok; ++n, ++g, ++c) {
@@ -542,37 +560,42 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
         for (int h = 0; h < 2; ++h) {
           const uint32_t at = aS + 64 * h;
           const int j = j0 + 64 * h;
+          const uint32_t mu = base + C::offScale + ((g & 3) * kBlk + 64 * h) * 4;
           if (!(ok = wait_warp<false>(&bars[bS + 2 * q + h], c & 1, abort_flag))) break;
           tc_fence_after();
           const uint32_t have = page_ok[g & 3] >> (4 * h) & 15u;
-          uint32_t x[32], y[32], pw[32];
           float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-          float all = 0.0f;
           bool done = have == 15u && j + 63 <= all_last && j >= all_lo && !__any_sync(0xffffffffu, live && M == -CUDART_INF_F);
           if (done) {
+            uint32_t x[32], y[32], pw[32];
             tmem_ld32p(at, x);
             arrived(x);
             tmem_ld32p(at + 32, y);
-            weigh(x, pw, M, sum);
+            weigh32(x, mu, pw, sum);
             arrived(y);
-            weigh(y, pw + 16, M, sum);
-            all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            weigh32(y, mu + 128, pw + 16, sum);
+            const float all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             done = __all_sync(0xffffffffu, !live || all <= kMostSum);
+            if (done) {
+              l += all;
+              tmem_st32p(at, pw);
+            }
           }
+          // The rare case in loops of 16 keys: unrolled, it took registers from the common one, which ran at
+          // four fifths of its speed.
           if (!done) {
-            tmem_ld32p(at, x);
-            tmem_ld32p(at + 32, y);
-            arrived(x);
-            reg_fence32(y);
-            mask(x, j, have);
-            mask(y, j + 32, have >> 2);
             // A mask alone needs no maximum where none can pass M by 2^15: |score| <= factor * d * mu.
             const volatile float* most = reinterpret_cast<volatile float*>(smem + C::offTop + (g & 3) * 16 + h * 8);
             const float mu_top = fmaxf(most[0], most[1]);
+            uint32_t x[16], y[8];
             if (!__all_sync(0xffffffffu, !live || cq * static_cast<float>(cv.d) * mu_top <= M + kMostLog2)) {
               float top = -CUDART_INF_F;
+#pragma unroll 1
+              for (int k = 0; k < 4; ++k) {
+                read16(at + 16 * k, j + 16 * k, have >> k & 1u, mu + 64 * k, x);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) top = fmax3(top, __uint_as_float(x[i]), __uint_as_float(y[i]));
+                for (int i = 0; i < 16; i += 2) top = fmax3(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+              }
               top *= cq;
               if (__any_sync(0xffffffffu, top > M + kSlack)) {
                 move_to(top, n, h);
@@ -580,13 +603,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
               }
             }
             sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-            const float ref = M == -CUDART_INF_F ? 0.0f : M;
-            weigh(x, pw, ref, sum);
-            weigh(y, pw + 16, ref, sum);
-            all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            // Upwards: the weights lie over scores that have been read.
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              read16(at + 16 * k, j + 16 * k, have >> k & 1u, mu + 64 * k, x);
+              const float ref = M == -CUDART_INF_F ? 0.0f : M;
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                y[i] = weigh(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), ref, sum[i & 1]);
+              tmem_st8(at + 8 * k, y);
+            }
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           }
-          l += all;
-          tmem_st32p(at, pw);
           tmem_st_wait();
           arrive(bP + 2 * q + h);
         }

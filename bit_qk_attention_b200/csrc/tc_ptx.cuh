@@ -163,20 +163,19 @@ __device__ __forceinline__ void mma_i8_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       : "memory");
 }
 
-// D[tmem] (+)= A[smem desc] * B[smem desc]; 16-bit float operands, fp32 accumulator. Without the
-// operand that disables output lanes: with it, even all zero, an instruction takes 96 cycles or more
-// (measured), without it 128 x 128 x 16 takes 64 and 128 x 64 x 16 takes 48 (A's read binds).
-__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// As mma_f8f6f4_ss without the operand that masks output lanes: with it the instruction takes 96 cycles or
+// more (measured), without it 128 x 64 x 32 takes 48 (the read of A binds).
+__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
-// As mma_f16_ss with A in tensor memory.
+// D[tmem] (+)= A[tmem] * B[smem desc]; 16-bit float operands, fp32 accumulator; no mask either.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                            uint32_t accumulate) {
   asm volatile(
