@@ -150,6 +150,7 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
 
 template <bool SLEEP>
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, wait_bar<SLEEP>(bar, parity, abort_flag));
 }
 
@@ -526,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
         reg_fence8(s + 8);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4 m = lds128(mu + 16 * i);
+          const uint4 m = *reinterpret_cast<const uint4*>(smem + mu + 16 * i);
           const uint32_t m4[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
           for (int e = 4 * i; e < 4 * i + 4; ++e)
@@ -541,11 +542,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
         const __half2 y = __floats2half2_rn(e.x, e.y);
         return *reinterpret_cast<const uint32_t*>(&y);
       };
-      // Of 32 keys with the scales at `mu`.
-      auto weigh32 = [&](const uint32_t (&s)[32], uint32_t mu, uint32_t* to, float2 (&sum)[2]) {
+      // Of sixteen keys with the scales at `mu`.
+      auto weigh16 = [&](const uint32_t (&s)[16], uint32_t mu, uint32_t* to, float2 (&sum)[2]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 m = lds128(mu + 16 * i);
+        for (int i = 0; i < 4; ++i) {
+          const uint4 m = *reinterpret_cast<const uint4*>(smem + mu + 16 * i);
           const float2 a = __fmul2_rn(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])),
                                       make_float2(__uint_as_float(m.x), __uint_as_float(m.y)));
           const float2 b = __fmul2_rn(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])),
@@ -554,26 +555,36 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
           to[2 * i + 1] = weigh(b, M, sum[1]);
         }
       };
+      bool fresh = true;  // a row has seen nothing yet
+      int owed = -1;      // half whose weights are on their way to tensor memory
+      auto hand_over = [&] {
+        tmem_st_wait();
+        arrive(bP + 2 * q + owed);
+      };
       for (int n = 0; n < n_blk && mine && ok; ++n, ++g, ++c) {
         const int j0 = w.block_at(v0 + n) * kBlk;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const uint32_t at = aS + 64 * h;
           const int j = j0 + 64 * h;
-          const uint32_t mu = base + C::offScale + ((g & 3) * kBlk + 64 * h) * 4;
+          const uint32_t mu = C::offScale + ((g & 3) * kBlk + 64 * h) * 4;
           if (!(ok = wait_warp<false>(&bars[bS + 2 * q + h], c & 1, abort_flag))) break;
           tc_fence_after();
+          uint32_t x[2][16];
+          tmem_ld16p(at, x[0]);
+          if (owed >= 0) hand_over();
           const uint32_t have = page_ok[g & 3] >> (4 * h) & 15u;
           float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-          bool done = have == 15u && j + 63 <= all_last && j >= all_lo && !__any_sync(0xffffffffu, live && M == -CUDART_INF_F);
+          bool done = have == 15u && j + 63 <= all_last && j >= all_lo && !fresh;
           if (done) {
-            uint32_t x[32], y[32], pw[32];
-            tmem_ld32p(at, x);
-            arrived(x);
-            tmem_ld32p(at + 32, y);
-            weigh32(x, mu, pw, sum);
-            arrived(y);
-            weigh32(y, mu + 128, pw + 16, sum);
+            uint32_t pw[32];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              tmem_ld_wait();
+              reg_fence16(x[k & 1]);
+              if (k < 3) tmem_ld16p(at + 16 * k + 16, x[(k + 1) & 1]);
+              weigh16(x[k & 1], mu + 64 * k, pw + 8 * k, sum);
+            }
             const float all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             done = __all_sync(0xffffffffu, !live || all <= kMostSum);
             if (done) {
@@ -587,14 +598,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
             // A mask alone needs no maximum where none can pass M by 2^15: |score| <= factor * d * mu.
             const volatile float* most = reinterpret_cast<volatile float*>(smem + C::offTop + (g & 3) * 16 + h * 8);
             const float mu_top = fmaxf(most[0], most[1]);
-            uint32_t x[16], y[8];
+            uint32_t z[16], y[8];
             if (!__all_sync(0xffffffffu, !live || cq * static_cast<float>(cv.d) * mu_top <= M + kMostLog2)) {
               float top = -CUDART_INF_F;
 #pragma unroll 1
               for (int k = 0; k < 4; ++k) {
-                read16(at + 16 * k, j + 16 * k, have >> k & 1u, mu + 64 * k, x);
+                read16(at + 16 * k, j + 16 * k, have >> k & 1u, mu + 64 * k, z);
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) top = fmax3(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                for (int i = 0; i < 16; i += 2) top = fmax3(top, __uint_as_float(z[i]), __uint_as_float(z[i + 1]));
               }
               top *= cq;
               if (__any_sync(0xffffffffu, top > M + kSlack)) {
@@ -606,19 +617,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
             // Upwards: the weights lie over scores that have been read.
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
-              read16(at + 16 * k, j + 16 * k, have >> k & 1u, mu + 64 * k, x);
+              read16(at + 16 * k, j + 16 * k, have >> k & 1u, mu + 64 * k, z);
               const float ref = M == -CUDART_INF_F ? 0.0f : M;
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                y[i] = weigh(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), ref, sum[i & 1]);
+                y[i] = weigh(make_float2(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1])), ref, sum[i & 1]);
               tmem_st8(at + 8 * k, y);
             }
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            fresh = __any_sync(0xffffffffu, live && M == -CUDART_INF_F);
           }
-          tmem_st_wait();
-          arrive(bP + 2 * q + h);
+          owed = h;
         }
       }
+      if (owed >= 0) hand_over();
       if (!ok) break;
       // The next (tile, head)'s scores can be made while this one's rows are written.
       if (write_next) cq_next = write_q(k);
