@@ -17,16 +17,15 @@ constexpr int64_t kMaxRows = (int64_t{1} << 31) - 4096;  // (token, head) rows o
 constexpr int64_t kMaxKv = int64_t{1} << 28;
 // Rows (new tokens x heads of a group) of a sequence up to which the decoding kernel is taken, with a
 // pass over the cache for every 16 rows (8 KV heads, d = 128, decoding kernel and the other one, us):
-//              1 x 8192 keys  32 x 4096  128 x 1024
-//   16 rows       18   41       49  186    79  194
-//   32 rows       19   42      101  186   140  195
-//   48 rows       20   42      141  187   199  199
-//   64 rows       23   42      180  187   260  200
-constexpr int kDecodeRows = 48;
+//              1 x 8192 keys  32 x 4096  128 x 1024  16 x 1024
+//   16 rows       18   36       49  126    79  141     16   24
+//   32 rows       20   36      100  126   139  142     20   24
+//   48 rows       20   37      139  127   201  145     41   24
+constexpr int kDecodeRows = 32;
 // Up to so many where its tiles fit on the GPU at once and a warp has at most so many blocks of 64 keys:
-// there the other kernel's start, cuts and join last longer than the further passes. 128 rows: 1 x 8192
-// keys (7 blocks) 30 and 44 us; 4 heads of 2 x 16384 (14 blocks) 48 and 57; 8 heads of 1 x 65536 (55
-// blocks) 149 and 100. 64 rows, 16 x 1024 keys, twice as many tiles as fit: 48 and 30.
+// there the other kernel's start, cuts and join last longer than the further passes. 48 rows, 1 x 65536
+// keys (21 blocks a warp) 66 and 76 us, 64 rows (28 blocks) 82 and 76; 128 rows, 1 x 8192 keys (7 blocks)
+// 29 and 40 us. 64 rows, 16 x 1024 keys, twice as many tiles as fit: 48 and 24.
 constexpr int kDraftRows = 128, kDraftBlocks = 24;
 constexpr int kChunkRows = 256;  // row tile of the kernel for more
 constexpr int64_t kMaxCtas = (int64_t{1} << 31) - 1;

@@ -3,29 +3,32 @@
 // 256 rows (new tokens x query heads of a group, which share every key) of one sequence and KV head
 // meet the 128-key blocks that any of them sees, as two tiles of 128 rows. The products run on tcgen05
 // with fp32 accumulators in tensor memory:
-//   S = Q K^T  bf16: Q is +-1, K is +-mu_j, so S = mu_j (d - 2 popc) comes out exact
-//   O += P V   fp16: P = 2^(s - M), V = code 2^e, both numbers of the cache exact in their type
+//   S = Q K^T  e4m3, both +-1: the whole number d - 2 popc comes out exact; mu_j follows in the softmax
+//   O += P V   fp16: P = 2^(s - M), rounded to fp16, V = code 2^e, exact in that type
 // One CTA per SM (it owns all tensor memory) walks its stretch of the line of all key blocks, so that
 // every SM has the same number of them whatever the lengths and the mask are:
 //   * The cache holds K in bits and V in bytes. One warp brings a block's rows by TMA (V through a
 //     swizzled tensor map); four expanding warps, one key per lane, read them into registers, which
-//     frees the stage for the next block, and write the 16-bit operands: two instructions per pair of K
-//     channels (the pair is (c, c + 16), so that one shift and one mask place both signs; Q has the
-//     same order, and a dot product does not mind), seven per four V channels. K and V operands are
-//     double-buffered.
-//   * Two warpgroups of softmax, one per tile, one thread per row. Most blocks take one pass, without a
-//     maximum: the weights 2^(s - M) are made with the M of the blocks before, and their sum, which is
+//     frees the stage for the next block, and write the operands: two instructions per four K channels,
+//     seven per four V channels. K and V operands are double-buffered. (K as +-mu_j in bf16 needed no
+//     product in the softmax, but twice the instructions, MMAs and shared memory: 1.03 ms, see below,
+//     instead of 0.97.)
+//   * Two warpgroups of softmax, one per tile, one thread per row. Most scores are read once, without a
+//     maximum: the weights 2^(s - M) are made with the M of the keys before, and their sum, which is
 //     needed anyway, shows whether any of them grew too large for fp16 (weights are positive: a sum up
-//     to 2^15 has none above). Only then, and in a row's first block, the scores are read twice, M moves
-//     to the maximum if that is 2^8 above it, and O is rescaled in tensor memory.
-//   * A block's scores come in two halves of 64 keys, so that a softmax warpgroup hardly waits for its
-//     own MMAs: the first half of the next block is issued as soon as this block's first half is done;
-//     its weights are made, and kept in registers, while P V and the second half of the scores run,
-//     which P's place (the second half of S) keeps apart.
+//     to 2^15 has none above). Only then, in a row's first keys and behind a mask, the scores are read
+//     again, M moves to the maximum if that is 2^8 above it, and O is rescaled in tensor memory.
+//   * A block's scores come in two halves of 64 keys, each with its weights over it: a half's P V and
+//     the scores two halves on follow its weights in the order of issue, while the softmax works on the
+//     other half. It reads the next half's first scores before it waits for its weights to arrive.
 //   * At the end of a (tile, head) a softmax warpgroup writes the next one's Q before it reads O, so that
 //     the next scores are made meanwhile.
-// A block of 256 x 128 scores costs 2048 cycles of exponentials (16 per cycle and SM) and as many
-// of MMAs at d = 128 (4096 products per cycle); that is the bound.
+// A block of 256 x 128 scores at d = 128 costs 2048 cycles of exponentials (16 per cycle and SM), and
+// 1792 of MMAs; that is the bound. A block takes about 4000: 4096 new tokens of 16 heads over 32768 keys
+// of 4 heads take 880 us (1.17 PFLOP/s). What it spends beyond the exponentials is the softmax warps' own
+// latency, two of them per scheduler: without any expanding or MMAs they take 850 us. (Four softmax
+// warpgroups, two per tile, with 80 registers a thread and a vote between them per half, took 1.05 ms;
+// asking for the next half's scores before the half is done 1.01.)
 //
 // Every wait is bounded (1 s): on expiry the kernel records a timeout in a device status word, all
 // roles leave, copies and MMAs in flight are waited for, and tensor memory is freed.
@@ -48,9 +51,11 @@ using namespace ptx;
 
 constexpr int kBlk = 128;      // keys per block: N of QK, K of PV
 constexpr int kTile = 128;     // rows per tile: M
-constexpr int kCost = 2;       // blocks that a CTA could do while it starts and ends a (tile, head)
-constexpr int kWholeBlocks = 6;  // blocks that cutting a (tile, head) has to save
-constexpr int kMinUnits = 4;   // units (blocks, and kCost) a CTA takes at least
+// Blocks that a CTA could do while it starts and ends a (tile, head): with 1, 2, 4 and 6 a prompt of 2 x
+// 8192 tokens in a window took 235, 201, 199 and 200 us, chunks of 4 x 1000 over 9000 keys 192, 189, 180, 180.
+constexpr int kCost = 4;
+constexpr int kWholeBlocks = 10; // blocks that cutting a (tile, head) has to save
+constexpr int kMinUnits = 6;   // units (blocks, and kCost) a CTA takes at least
 constexpr int kThreads = 512;  // service, expanding and two softmax warpgroups
 constexpr float kSlack = 8.0f;        // log2 by which a block's maximum may pass M
 constexpr float kMostLog2 = 15.0f;    // log2 of weights that fp16 surely holds
@@ -743,7 +748,8 @@ void paged_chunk_plan(PagedAttnParams* p, int sms) {
   const int64_t blocks = most_blocks(*p, p->row_tile, kBlk), tiles = static_cast<int64_t>(p->B) * p->row_tiles * p->cache.heads;
   p->cluster = 1;
   // Cutting (tile, head)s to fill the GPU costs what kWholeBlocks blocks do (finding the cuts, and the
-  // second launch): 80 of 12 blocks took 41 us whole and 49 us cut, 80 of 16 blocks 52 us either way.
+  // second launch): 80 of 12 blocks took 38 us whole and 58 us cut, 80 of 23 blocks 62 and 73 us, 8 of 8
+  // blocks 27 and 31 us, but 8 of 16 blocks 42 and 35 us.
   const int64_t even = std::max<int64_t>((blocks + kCost) * tiles / sms, kMinUnits - kCost);
   p->whole = tiles <= sms && blocks - even <= kWholeBlocks ? 1 : 0;
   p->ctas = p->whole ? static_cast<int>(tiles) : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, (blocks + kCost) * tiles / kMinUnits)));

@@ -273,7 +273,7 @@ ba_status ba_cache_read(const ba_kv_cache* cache, const int64_t* slots, int64_t 
  *   mu_q = mean |q| of the row in fp32;  o = sum_j exp(s_j) v^_j / sum_j exp(s_j),
  *   lse = log sum_j exp(s_j).
  * There is no 8-bit P here. For many rows the weights are rounded to fp16 (relative 2^-11) for the
- * product with V, which accumulates in fp32. For few rows (max_q_len * G up to 48, or 128 where there
+ * product with V, which accumulates in fp32. For few rows (max_q_len * G up to 32, or 128 where there
  * is little work) they are rounded to 16 bits below the largest weight * 2^e of 64 keys (2^-17 of it), products are exact and their
  * sums of 64 keys are added in fp32. Scores, maxima and sums are fp32. A row that sees nothing gets
  * o = 0 and lse = -inf.
