@@ -404,87 +404,69 @@ class KVCache:
         return self._c
 
 
-# The entry points below run many times per second on small tensors, so their checks are written for
-# little Python. What they allocate, and their kernels, belong to the current stream of the cache's
-# device; a call for another stream, or from another current device, is made again inside of it.
-def _elsewhere(dev: int, stream) -> bool:
-    return stream is not None or dev != _torch()._C._cuda_getDevice()
+# The entry points below run many times per second on small tensors, so their checks, allocations and C calls
+# are made by a compiled module (csrc/paged_binding.cpp). What they allocate, and their kernels, belong to the
+# current stream of the cache's device; a call for another stream, or from another current device, is made
+# again inside of it.
+_module = None
 
 
-def _on(cache, stream):
+def _native():
+    global _module
+    if _module is None:
+        L = lib()
+        _torch()
+        try:
+            from . import _paged
+        except ImportError as e:
+            raise RuntimeError("the module _paged has not been built for this interpreter: build it with "
+                               "`python -m bit_qk_attention_b200.build`") from e
+        _paged.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+            "ba_kv_block_bytes", "ba_cache_write", "ba_cache_read", "ba_paged_workspace_bytes", "ba_attention_paged")))
+        _module = _paged
+    return _module
+
+
+def _elsewhere(cache, dev: int, stream):
+    """The context in which a call has to be made again, or None."""
     torch = _torch()
-    if stream is None:
-        return torch.cuda.device(cache.data.device)
-    if stream.device != cache.data.device:
-        raise ValueError("stream and cache must be on one device")
-    return torch.cuda.stream(stream)
-
-
-def _check_index(t, name: str, dtype, dev: int, shape):
-    if t.dtype != dtype or t.get_device() != dev or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on the cache's device")
-
-
-def _check_rows(t, name: str, dev: int, heads, d: int) -> int:
-    """Checks rows [tokens, heads, d] of 16-bit numbers; returns their ba_dtype."""
-    torch = _torch()
-    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [tokens, heads, {d}] with the cache's heads")
-    if t.stride(2) != 1 and d > 1 and t.numel() > 0:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on the cache's device")
-    dt = t.dtype
-    if dt == torch.bfloat16:
-        return BA_BF16
-    if dt == torch.float16:
-        return BA_F16
-    raise ValueError(f"{name} must be fp16 or bf16")
+    if dev < 0:
+        raise ValueError("cache data must be a contiguous uint8 CUDA tensor [pages, heads, block bytes]")
+    if stream is not None:
+        if stream.device != cache.data.device:
+            raise ValueError("stream and cache must be on one device")
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(dev) if dev != torch._C._cuda_getDevice() else None
 
 
 def cache_write(cache: KVCache, k, v, slots, stream=None) -> None:
     """Quantise new rows k, v [T, n_kv_heads, d] (fp16/bf16; strided views are taken as they are)
     and write them to the tokens at slots (int64 [T], page * page_size + offset; -1 skips a row).
     Slots in range must differ."""
-    torch = _torch()
-    cc = cache.c()
-    dev = cache.data.get_device()
-    if _elsewhere(dev, stream):
-        with _on(cache, stream):
+    data = cache._data
+    dev = data.get_device()
+    other = _elsewhere(cache, dev, stream)
+    if other is not None:
+        with other:
             return cache_write(cache, k, v, slots)
-    dt = _check_rows(k, "k", dev, cc.n_kv_heads, cc.d)
-    if _check_rows(v, "v", dev, cc.n_kv_heads, cc.d) != dt or v.shape[0] != k.shape[0]:
-        raise ValueError("k and v must share dtype and shape")
-    T = k.shape[0]
-    _check_index(slots, "slots", torch.int64, dev, (T,))
-    kt, kh, _ = k.stride()
-    vt, vh, _ = v.stride()
-    _check(lib().ba_cache_write(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, dt, T, slots.data_ptr(),
-                                ctypes.byref(cc), torch._C._cuda_getCurrentRawStream(dev)), "ba_cache_write")
+    _check(_native().write(data, cache._page_size, cache._d, k, v, slots, _torch()._C._cuda_getCurrentRawStream(dev)),
+           "ba_cache_write")
 
 
 def cache_read(cache: KVCache, slots, dtype=None, k_out=None, v_out=None, stream=None) -> Tuple[object, object]:
     """(k, v) [T, n_kv_heads, d]: the rows at slots (int64 [T]) as numbers; rows out of range are 0.
     dtype: fp16, bf16 (default) or fp32, or that of k_out / v_out where they are given."""
-    torch = _torch()
-    cc = cache.c()
-    dev = cache.data.get_device()
-    if _elsewhere(dev, stream):
-        with _on(cache, stream):
+    data = cache._data
+    dev = data.get_device()
+    other = _elsewhere(cache, dev, stream)
+    if other is not None:
+        with other:
             return cache_read(cache, slots, dtype, k_out, v_out)
-    T = slots.numel()
-    _check_index(slots, "slots", torch.int64, dev, (T,))
-    shape = (T, cc.n_kv_heads, cc.d)
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is not None:
-            dtype = dtype or t.dtype
-            _check_index(t, name, dtype, dev, shape)
-    dtype = dtype or torch.bfloat16
-    k = slots.new_empty(shape, dtype=dtype) if k_out is None else k_out
-    v = torch.empty_like(k) if v_out is None else v_out
-    _check(lib().ba_cache_read(ctypes.byref(cc), slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), _dt(k),
-                               torch._C._cuda_getCurrentRawStream(dev)), "ba_cache_read")
-    return k, v
+    r = _native().read(data, cache._page_size, cache._d, slots, dtype, k_out, v_out,
+                       _torch()._C._cuda_getCurrentRawStream(dev))
+    if r.__class__ is int:
+        _check(r, "ba_cache_read")
+    return r
 
 
 def attention_paged(q, cache: KVCache, page_table, kv_lens, cu_seqlens_q=None, max_q_len: Optional[int] = None,
@@ -505,57 +487,19 @@ def attention_paged(q, cache: KVCache, page_table, kv_lens, cu_seqlens_q=None, m
     Returns o [T, n_heads, d] (out_dtype, default q's; rows of no sequence are left as they were in
     `out`), and with return_lse also the fp32 log of the softmax sums [T, n_heads].
     """
-    torch = _torch()
-    cc = cache.c()
-    dev = cache.data.get_device()
-    if _elsewhere(dev, stream):
-        with _on(cache, stream):
+    data = cache._data
+    dev = data.get_device()
+    other = _elsewhere(cache, dev, stream)
+    if other is not None:
+        with other:
             return attention_paged(q, cache, page_table, kv_lens, cu_seqlens_q, max_q_len, max_kv_len, causal, window,
                                    sinks, softmax_scale, out, out_dtype, return_lse, workspace)
-    dt = _check_rows(q, "q", dev, None, cc.d)
-    T, heads, _ = q.shape
-    B = kv_lens.numel()
-    _check_index(kv_lens, "kv_lens", torch.int32, dev, (B,))
-    cu = 0
-    if cu_seqlens_q is not None:
-        _check_index(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev, (B + 1,))
-        cu = cu_seqlens_q.data_ptr()
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B or \
-            (page_table.stride(1) != 1 and page_table.shape[1] > 1) or page_table.get_device() != dev:
-        raise ValueError("page_table must be an int32 tensor [sequences, pages] on the cache's device, contiguous in "
-                         "its last dimension")
-    pages = page_table.shape[1]
-    if max_q_len is None:
-        max_q_len = 1 if cu_seqlens_q is None else T
-    if max_kv_len is None:
-        max_kv_len = pages * cc.page_size
-    if out is not None:
-        _check_index(out, "out", out_dtype or out.dtype, dev, (T, heads, cc.d))
-        odt = _dt(out)
-    else:
-        out = torch.empty_like(q, dtype=out_dtype, memory_format=torch.contiguous_format)
-        odt = dt if out_dtype is None else _dt(out)
-    lse = q.new_empty((T, heads), dtype=torch.float32) if return_lse else None
-    L = lib()
-    # Larger numbers than a C int holds mean the same as the largest.
-    max_q_len, window, sinks = min(max_q_len, 0x7fffffff), min(window, 0x7fffffff), min(sinks, 0x7fffffff)
-    max_kv_len = min(max_kv_len, pages * cc.page_size)
-    sq = CPagedSeqs(B, T, heads, max_q_len, max_kv_len, cu, kv_lens.data_ptr(), page_table.data_ptr(),
-                    page_table.stride(0), pages, 1 if causal else 0, window, sinks)
-    c_cache, c_seqs = ctypes.byref(cc), ctypes.byref(sq)
-    nws = L.ba_paged_workspace_bytes(c_cache, c_seqs)
-    if workspace is None:
-        # (size_t) -1 stands for arguments that the call below refuses.
-        if 0 < nws != ctypes.c_size_t(-1).value:
-            workspace = kv_lens.new_empty((nws,), dtype=torch.uint8)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the cache's device")
-    qt, qh, _ = q.stride()
-    _check(L.ba_attention_paged(q.data_ptr(), qt, qh, dt, c_cache, c_seqs, softmax_scale, out.data_ptr(), odt,
-                                0 if lse is None else lse.data_ptr(), 0 if workspace is None else workspace.data_ptr(),
-                                0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                torch._C._cuda_getCurrentRawStream(dev)), "ba_attention_paged")
-    return (out, lse) if return_lse else out
+    r = _native().attend(data, cache._page_size, cache._d, q, page_table, kv_lens, cu_seqlens_q, max_q_len, max_kv_len,
+                         causal, window, sinks, softmax_scale, out, out_dtype, return_lse, workspace,
+                         _torch()._C._cuda_getCurrentRawStream(dev))
+    if r.__class__ is int:
+        _check(r, "ba_attention_paged")
+    return r
 
 
 def bias_from_workload(w, device) -> Optional[Bias]:

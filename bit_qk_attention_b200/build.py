@@ -1,9 +1,10 @@
-"""Builds libbinattn.so (the C-ABI library) in-tree for sm_100a with nvcc."""
+"""Builds libbinattn.so (the C-ABI library, for sm_100a with nvcc) and _paged.so (a Python module) in-tree."""
 from __future__ import annotations
 
 import glob
 import os
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -12,7 +13,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbinattn.so")
+MODULE = os.path.join(PKG, "_paged.so")
+MODULE_SRC = os.path.join(CSRC, "paged_binding.cpp")
 NVCC = os.environ.get("NVCC", "nvcc")
+CXX = os.environ.get("CXX", "g++")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
@@ -33,7 +37,27 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def build_module(force: bool = False) -> str:
+    """The Python module of the paged cache's entry points, against this interpreter's torch."""
+    deps = [MODULE_SRC, os.path.join(INCLUDE, "binattn.h")]
+    if not force and os.path.exists(MODULE) and all(os.path.getmtime(f) <= os.path.getmtime(MODULE) for f in deps):
+        return MODULE
+    import torch
+    home = os.path.dirname(os.path.abspath(torch.__file__))
+    tmp = MODULE + f".tmp{os.getpid()}"
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(home, "include"), "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", MODULE_SRC, "-o", tmp,
+           "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CXX} failed for {MODULE_SRC}:\n{r.stderr}")
+    os.replace(tmp, MODULE)
+    return MODULE
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    build_module(force)
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -142,3 +142,23 @@ def test_workspace_does_not_grow_past_the_window(ba):
     one = lambda **kw: L.ba_paged_workspace_bytes(ctypes.byref(_cache(ba)), ctypes.byref(_seqs(ba, B=1, T=1, max_q_len=1, max_pages=1 << 16, **kw)))
     assert one(max_kv_len=1 << 20, window=64) == 0
     assert one(max_kv_len=128) == 0 and one(max_kv_len=0) == 0 and one(max_kv_len=1 << 20) > 0
+
+
+def test_python_calls_refuse_what_they_cannot_take(ba):
+    """Before anything reaches a device: a cache that is not on one, arguments that are no tensors or numbers."""
+    c = ba.KVCache.zeros(1, 1, 64, device="cpu")
+    rows, idx = torch.zeros(1, 1, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int64)
+    for call in (lambda: ba.cache_write(c, rows, rows, idx), lambda: ba.cache_read(c, idx),
+                 lambda: ba.attention_paged(rows, c, idx[None].int(), idx.int())):
+        with pytest.raises(ValueError):
+            call()
+    m = ba._native()
+    for args in ((), (c.data,), (c.data, 64, 64, rows, rows, idx, 0, 0)):
+        with pytest.raises(TypeError):
+            m.write(*args)
+    with pytest.raises(TypeError):
+        m.write(None, 64, 64, rows, rows, idx, 0)
+    with pytest.raises(ValueError):
+        m.write(c.data, 64, 64, rows, rows, idx, 0)
+    with pytest.raises(ValueError):
+        m.read(c.data, 64, 64, idx, None, None, None, 0)
