@@ -366,22 +366,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
           const uint32_t vote = __ballot_sync(0xffffffffu, page >= 0 && piece < per) & 0x11111111u;
           const uint32_t have = __ballot_sync(0xffffffffu, lane < 8 && (vote >> (4 * (lane * kPageUnit / unit))) & 1u);
           if (g > 0 && !(ok = wait_warp<true>(&bars[bRawEmpty], (g - 1) & 1, abort_flag))) break;
+          // No page: the rows are not seen, but what they are made into stays finite. These zeros come before
+          // the arrival, which may complete the phase by itself.
+          if (piece < per && page < 0 && kind > 0)
+            for (int i = 0; i < unit / 16 * xsize; ++i) sts128(extra + 16 * i, 0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
           if (lane == 0) {
             page_ok[g & 3] = have;
             mbar_arrive_expect_tx(&bars[bRawFull], __popc(vote) * unit * C::kToken);
           }
-          fence_proxy_async_smem();
           __syncwarp();
-          if (piece < per) {
-            if (page < 0) {
-              // No page: the rows are not seen, but what their scores are made of stays finite.
-              if (kind > 0)
-                for (int i = 0; i < unit / 16 * xsize; ++i) sts128(extra + 16 * i, 0u, 0u, 0u, 0u);
-            } else if (kind == 0) {
+          if (piece < per && page >= 0) {
+            if (kind == 0)
               tma_load_3d(base + C::offRaw + unit * piece * C::kRow, &v_map, bar, 0, off, page * cv.heads + k.head);
-            } else {
+            else
               bulk_load(extra, cv.block(page, k.head) + xoff + off * xsize, unit * xsize, bar);
-            }
           }
           __syncwarp();
         }

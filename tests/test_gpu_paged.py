@@ -428,6 +428,22 @@ def test_garbage_on_pages_before_the_window(ba, qn):
     _compare(*_run(ba, prob, **kw), _ref(ba, prob, **kw))
 
 
+@pytest.mark.parametrize("qn", [[1], [60]])
+def test_missing_pages_behind_garbage(ba, qn):
+    """A whole block without pages after one whose rows before the window hold garbage: none of that is left over."""
+    ps, n = 16, 384
+    window = n - qn[0] - 100 + 1  # the first key that any row sees is 100
+    c, q, table, kv, cu = _problem(ba, qn, [n], 4, 1, 128, ps, "bf16", 35)
+    for j in range(100 // ps):
+        c.data[int(table[0, j])] = 0x80
+        c.v_exp[int(table[0, j])] = 127
+    table[0, 128 // ps:256 // ps] = -1
+    prob = (c, q, table, kv, cu)
+    for _ in range(20):
+        got = _run(ba, prob, window=window)
+    _compare(*got, _ref(ba, prob, window=window))
+
+
 @pytest.mark.parametrize("qn", [[1], [40], [80]])
 def test_negative_scales_behind_a_sequence_that_ends_in_its_largest_keys(ba, qn):
     """The last, partly filled block has scores far above all before: what lies behind it must not hide that."""
