@@ -52,8 +52,8 @@ def visible(p, n, causal, window, sinks):
 def attend(q, block, ps, d, table, kv_lens, cu, causal=True, window=0, sinks=0, scale=0.0, eps_out=0.0):
     """(o, lse, tolerance of o, tolerance of lse) for q [T, Hq, d]; rows of no sequence are NaN.
 
-    The tolerances count the kernels' roundings. A weight carries half a step of fp16 (2^-11) twice (once when it is
-    made, and once more if its row's reference moves before it is used) and the error of its exponent: scores are a few fp32 products of at most max|s|, together within 2^-19 (1 + max|s|). Weights below
+    The tolerances count the kernels' roundings. A weight carries half a step of fp16 (2^-11) and the error of its
+    exponent: scores are a few fp32 products of at most max|s|, together within 2^-19 (1 + max|s|). Weights below
     fp16's normal range are off by at most 2^-25 of the largest weight's unit, times a code of at most 127 in the
     largest exponent. The product adds n / 16 partial sums in fp32. The output rounds once.
     With few rows the weights are fixed-point numbers instead, in units of 1 / 65280 of the largest w_j 2^e_j of a
@@ -95,7 +95,7 @@ def attend(q, block, ps, d, table, kv_lens, cu, causal=True, window=0, sinks=0, 
                 big, m = float(s.abs().max()), int(see.sum())
                 up = 2.0 ** int(e[see, h // G].max())
                 A = w @ vv.abs()
-                to[t0 + i, h] = A * (2.0 ** -10 + 2.0 ** -18 * (1 + big) + (m / 16) * 2.0 ** -23) \
+                to[t0 + i, h] = A * (2.0 ** -11 + 2.0 ** -18 * (1 + big) + (m / 16) * 2.0 ** -23) \
                     + m * 2.0 ** -25 * 127 * up \
                     + m * 127 * 0.5 / 65280 * float((w * 2.0 ** e[see, h // G].to(F64)).max()) + o[t0 + i, h].abs() * eps_out / 2 * (1 + 2.0 ** -10)
                 tl[t0 + i, h] = 2.0 ** -19 * (1 + big) + m * 2.0 ** -26
