@@ -79,7 +79,7 @@ struct Cfg {
   static constexpr int kToken = kRow + 16 + 2 + 1;  // bytes that a token brings
   static constexpr int kNumBars = 26;
   static constexpr int offMisc = offBar + kNumBars * 8;  // tensor memory base, abort flag, page masks [4]
-  static constexpr int offTop = offMisc + 8 + 16;  // [block % 4][expanding warp]: largest mu of its keys
+  static constexpr int offTop = offMisc + 8 + 16;  // [block % 4][expanding warp]: bits of the largest mu of its keys
   static constexpr int offScratch = offTop + 64;
   static constexpr int kBytes = offScratch + (kThreads / 32 + 2) * 8;
   static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
@@ -402,9 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
         const uint4 bits = lds128(base + C::offBits + row * 16);
         const uint32_t mu = lds16(base + C::offMu + row * 2);
         const int e8 = static_cast<int8_t>(lds16(base + C::offExp + (row & ~1)) >> (8 * (row & 1)));
-        // A row behind the sequence may hold a negative mu: its sign would hide the others.
+        // A row that nobody sees may hold a negative mu, whose sign would hide the others, or NaN: as whole
+        // numbers, bits without a sign have the order of what they stand for, with NaN above all.
         const uint32_t mu_top = __reduce_max_sync(0xffffffffu, mu & 0x7fffu);
-        if (lane == 0) *reinterpret_cast<volatile float*>(smem + C::offTop + (g & 3) * 16 + (warp - 4) * 4) = __uint_as_float(mu_top << 16);
+        if (lane == 0) *reinterpret_cast<volatile uint32_t*>(smem + C::offTop + (g & 3) * 16 + (warp - 4) * 4) = mu_top << 16;
         *reinterpret_cast<volatile float*>(smem + C::offScale + ((g & 3) * kBlk + row) * 4) = __uint_as_float(mu << 16);
         uint4 code[CH / 16];
 #pragma unroll
@@ -600,9 +601,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
           // The rare case in loops of 16 keys: unrolled, it took registers from the common one, which ran at
           // four fifths of its speed.
           if (!done) {
-            // A mask alone needs no maximum where none can pass M by 2^15: |score| <= factor * d * mu.
-            const volatile float* most = reinterpret_cast<volatile float*>(smem + C::offTop + (g & 3) * 16 + h * 8);
-            const float mu_top = fmaxf(most[0], most[1]);
+            // A mask alone needs no maximum where none can pass M by 2^15: |score| <= factor * d * mu. A NaN
+            // among the half's scales, seen or not, fails the comparison.
+            const volatile uint32_t* most = reinterpret_cast<volatile uint32_t*>(smem + C::offTop + (g & 3) * 16 + h * 8);
+            const float mu_top = __uint_as_float(max(most[0], most[1]));
             uint32_t z[16], y[8];
             if (!__all_sync(0xffffffffu, !live || cq * static_cast<float>(cv.d) * mu_top <= M + kMostLog2)) {
               float top = -CUDART_INF_F;
