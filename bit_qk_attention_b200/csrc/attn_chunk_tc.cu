@@ -4,7 +4,8 @@
 // meet the 128-key blocks that any of them sees, as two tiles of 128 rows. The products run on tcgen05
 // with fp32 accumulators in tensor memory:
 //   S = Q K^T  e4m3, both +-1: the whole number d - 2 popc comes out exact; mu_j follows in the softmax
-//   O += P V   fp16: P = 2^(s - M), rounded to fp16, V = code 2^e, exact in that type
+//   O += P V   fp16: P = 2^(s - M), rounded to fp16, V = code 2^e, exact in that type. M is 2^3 to 2^7 below the
+//              largest score, not at it: fp16 then loses precision only 2^17 to 2^21 below the largest weight
 // One CTA per SM (it owns all tensor memory) walks its stretch of the line of all key blocks, so that
 // every SM has the same number of them whatever the lengths and the mask are:
 //   * The cache holds K in bits and V in bytes. One warp brings a block's rows by TMA (V through a
@@ -16,8 +17,9 @@
 //   * Two warpgroups of softmax, one per tile, one thread per row. Most scores are read once, without a
 //     maximum: the weights 2^(s - M) are made with the M of the keys before, and their sum, which is
 //     needed anyway, shows whether any of them grew too large for fp16 (weights are positive: a sum up
-//     to 2^15 has none above). Only then, in a row's first keys and behind a mask, the scores are read
-//     again, M moves to the maximum if that is 2^8 above it, and O is rescaled in tensor memory.
+//     to 65504 has none above). Only then, in a row's first keys and behind a mask, the scores are read
+//     again, M moves to 2^3 to 2^7 below the maximum if that is 2^9.9 above it, and O is rescaled in tensor
+//     memory.
 //   * A block's scores come in two halves of 64 keys, each with its weights over it: a half's P V and
 //     the scores two halves on follow its weights in the order of issue, while the softmax works on the
 //     other half. It reads the next half's first scores before it waits for its weights to arrive.
@@ -57,9 +59,15 @@ constexpr int kCost = 4;
 constexpr int kWholeBlocks = 10; // blocks that cutting a (tile, head) has to save
 constexpr int kMinUnits = 6;   // units (blocks, and kCost) a CTA takes at least
 constexpr int kThreads = 512;  // service, expanding and two softmax warpgroups
-constexpr float kSlack = 8.0f;        // log2 by which a block's maximum may pass M
-constexpr float kMostLog2 = 15.0f;    // log2 of weights that fp16 surely holds
-constexpr float kMostSum = 32768.0f;  // a sum of weights up to this has none above it
+// Weights are 2^(s - M), and M is set some way below the largest score, so that fp16 has its full precision down
+// to 2^-14 of 1, not of the largest weight, and steps of 2^-24 below: kBelow, or less (kLeastBelow at least) where
+// the bound on a masked half's scores would then pass kMostLog2 and its maximum be read for nothing (7 always: a
+// prompt of 2 x 8192 tokens in a window took 205.5 us instead of 202.2). M moves where a maximum would reach 2^kHigh:
+// 64 weights up to that sum to less than kMostSum, so a half whose sum is larger always moves it.
+constexpr float kBelow = 7.0f, kLeastBelow = 3.0f;
+constexpr float kHigh = 9.9f;
+constexpr float kMostLog2 = 15.9f;    // log2 of weights that fp16 surely holds
+constexpr float kMostSum = 65504.0f;  // fp16's largest number: a sum of weights up to this has none above it
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 
 template <int CH>  // channels of the operands: 64 or 128 (>= d)
@@ -495,10 +503,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
       if (!mine) g += n_blk;
       // A score passes M by more than the slack: M moves, and what there is of the row is rescaled. O
       // holds the halves before half h of block n.
-      auto move_to = [&](float top, int n, int h) {
-        const bool moves = top > M + kSlack;
-        const float f = moves ? ex2_approx(M - top) : 1.0f;  // 0 for a row's first keys
-        if (moves) M = top;
+      auto move_to = [&](float top, float bound, int n, int h) {
+        const bool moves = top > M + kHigh;
+        // The bound may grow by 1 with the scales of the keys to come.
+        const float to = fminf(top - kLeastBelow, fmaxf(top - kBelow, bound + (1.0f - kMostLog2)));
+        const float f = moves ? ex2_approx(M - to) : 1.0f;  // 0 for a row's first keys
+        if (moves) M = to;
         l *= f;
         if (n + h > 0 && (ok = wait_warp<false>(&bars[bPV + 2 * q + 1 - h], (c - 1 + h) & 1, abort_flag))) {
           tc_fence_after();
@@ -601,12 +611,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
           // The rare case in loops of 16 keys: unrolled, it took registers from the common one, which ran at
           // four fifths of its speed.
           if (!done) {
-            // A mask alone needs no maximum where none can pass M by 2^15: |score| <= factor * d * mu. A NaN
+            // A mask alone needs no maximum where none can pass M by 2^15.9: |score| <= factor * d * mu. A NaN
             // among the half's scales, seen or not, fails the comparison.
             const volatile uint32_t* most = reinterpret_cast<volatile uint32_t*>(smem + C::offTop + (g & 3) * 16 + h * 8);
             const float mu_top = __uint_as_float(max(most[0], most[1]));
+            const float bound = cq * static_cast<float>(cv.d) * mu_top;
             uint32_t z[16], y[8];
-            if (!__all_sync(0xffffffffu, !live || cq * static_cast<float>(cv.d) * mu_top <= M + kMostLog2)) {
+            if (!__all_sync(0xffffffffu, !live || bound <= M + kMostLog2)) {
               float top = -CUDART_INF_F;
 #pragma unroll 1
               for (int k = 0; k < 4; ++k) {
@@ -615,8 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
                 for (int i = 0; i < 16; i += 2) top = fmax3(top, __uint_as_float(z[i]), __uint_as_float(z[i + 1]));
               }
               top *= cq;
-              if (__any_sync(0xffffffffu, top > M + kSlack)) {
-                move_to(top, n, h);
+              if (__any_sync(0xffffffffu, top > M + kHigh)) {
+                move_to(top, bound, n, h);
                 if (!ok) break;
               }
             }

@@ -272,8 +272,9 @@ ba_status ba_cache_read(const ba_kv_cache* cache, const int64_t* slots, int64_t 
  *   s_j = softmax_scale * mu_q * mu_j * (d - 2 popc(sign bits of q XOR sign bits of k_j)),
  *   mu_q = mean |q| of the row in fp32;  o = sum_j exp(s_j) v^_j / sum_j exp(s_j),
  *   lse = log sum_j exp(s_j).
- * There is no 8-bit P here. For many rows the weights are rounded to fp16 (relative 2^-11) for the
- * product with V, which accumulates in fp32. For few rows (max_q_len * G up to 32, or 128 where there
+ * There is no 8-bit P here. For many rows the weights are rounded to fp16 for the product with V,
+ * which accumulates in fp32: off by at most 2^-11 of themselves, or, far below the row's largest
+ * weight, 2^-28 of that one. For few rows (max_q_len * G up to 32, or 128 where there
  * is little work) they are rounded to 16 bits below the largest weight * 2^e of 64 keys (2^-17 of it), products are exact and their
  * sums of 64 keys are added in fp32. Scores, maxima and sums are fp32. A row that sees nothing gets
  * o = 0 and lse = -inf.

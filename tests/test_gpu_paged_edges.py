@@ -54,3 +54,43 @@ def test_nan_scales_before_a_window_that_begins_with_its_largest_keys(ba, qn):
     kw = dict(window=window, sinks=sinks)
     _compare(*_run(ba, prob, **kw), _ref(ba, prob, **kw))
 
+
+# ----------------------------------------------------------------------------- weights far below the largest
+@pytest.mark.parametrize("below", [20.5, 25.5])
+@pytest.mark.parametrize("qn", [1, 130])
+@pytest.mark.parametrize("large_scale", [False, True])
+def test_many_small_weights_beside_one_large(ba, large_scale, qn, below):
+    """One key holds nearly all of the mass, and its values are 0: o is what the others, each 2^-below of it, add up to.
+
+    With w = 2^-below and n - 1 keys of value 1 beside the large one, o = (n - 1) w / (1 + (n - 1) w). A weight
+    of the kernel for many rows is off by at most 2^-11 of itself or 2^-32 of the largest (2^-28 where a key's scale
+    would allow scores far above those there are). One of the kernel for
+    few rows is off by at most 2^-17 of the largest w 2^e of its 64 keys: beside the large key, whose values of 0 have
+    the exponent -24, that is 2^-9.5 of itself for 63 of n keys, else 2^-17. Scores are fp32 numbers up to 26, off
+    by at most 2^-19 (1 + 26), and o rounds once to fp32."""
+    d, ps, n = 64, 128, 16384
+    B = torch.cuda.get_device_properties(0).multi_processor_count  # as many (tile, head)s: none of them is cut
+    c = ba.KVCache.zeros(n // ps, 1, d, ps)
+    k = torch.ones((n, 1, d), dtype=torch.bfloat16)
+    k[1:, :, ::2] = -1.0  # half of the signs differ: score 0
+    if large_scale:
+        k[5] *= 64.0  # a score of 0 too
+    v = torch.ones_like(k)
+    v[0] = 0.0
+    ba.cache_write(c, k.cuda(), v.cuda(), torch.arange(n).cuda())
+    q = torch.ones((B * qn, 1, d), dtype=torch.bfloat16).cuda()
+    table = torch.arange(n // ps, dtype=torch.int32)[None].expand(B, -1).cuda()
+    kv = torch.full((B,), n, dtype=torch.int32).cuda()
+    cu = torch.arange(0, B * qn + 1, qn, dtype=torch.int32).cuda()
+    scale = below * math.log(2.0) / d
+    o, lse = ba.attention_paged(q, c, table, kv, cu, max_q_len=qn, causal=False, softmax_scale=scale,
+                                out_dtype=torch.float32, return_lse=True)
+    torch.cuda.synchronize()
+    ba.check_device_status()
+    mass = (n - 1) * 2.0 ** -below
+    want = mass / (1 + mass)
+    tol = want * (2.0 ** -11 + 2.0 ** -19 * 27 + 2.0 ** -23) + n * 2.0 ** (-28 if large_scale else -32)
+    assert ((o.double() - want).abs() <= tol).all(), (float((o.double() - want).abs().max()), tol)
+    want = below * math.log(2.0) + math.log1p(mass)
+    assert ((lse.double() - want).abs() <= 2.0 ** -19 * 27 + n * 2.0 ** -26).all()
+
