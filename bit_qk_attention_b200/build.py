@@ -4,6 +4,7 @@ from __future__ import annotations
 import glob
 import os
 import subprocess
+import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
@@ -37,12 +38,17 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
-def build_module(force: bool = False) -> str:
-    """The Python module of the paged cache's entry points, against this interpreter's torch."""
+def build_module(force: bool = False) -> str | None:
+    """The Python module of the paged cache's entry points, against this interpreter's torch; None where there is no
+    torch (the C library needs none)."""
+    try:
+        import torch
+    except ImportError as e:
+        print(f"no Python module of the paged cache's calls: {e}", file=sys.stderr)
+        return None
     deps = [MODULE_SRC, os.path.join(INCLUDE, "binattn.h")]
     if not force and os.path.exists(MODULE) and all(os.path.getmtime(f) <= os.path.getmtime(MODULE) for f in deps):
         return MODULE
-    import torch
     home = os.path.dirname(os.path.abspath(torch.__file__))
     tmp = MODULE + f".tmp{os.getpid()}"
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
@@ -57,7 +63,13 @@ def build_module(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    """The library, and then the Python module where torch is there."""
+    path = build_library(force, verbose, ptxas_info)
     build_module(force)
+    return path
+
+
+def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
@@ -112,5 +124,4 @@ def build_variant(tag: str, defines, force: bool = False) -> str:
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose=True, ptxas_info="--ptxas" in sys.argv))
