@@ -415,12 +415,15 @@ def _native():
     global _module
     if _module is None:
         L = lib()
-        _torch()
+        torch = _torch()
         try:
             from . import _paged
-        except ImportError as e:
-            raise RuntimeError("the module _paged has not been built for this interpreter: build it with "
-                               "`python -m bit_qk_attention_b200.build`") from e
+            built_for = getattr(_paged, "built_for", "another torch")
+        except ImportError:
+            built_for = "nothing here"
+        if built_for != "torch " + torch.__version__:
+            raise RuntimeError(f"the module _paged has been built for {built_for}, and this is torch {torch.__version__}: "
+                               "build it with `python -m bit_qk_attention_b200.build`")
         _paged.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
             "ba_kv_block_bytes", "ba_cache_write", "ba_cache_read", "ba_paged_workspace_bytes", "ba_attention_paged")))
         _module = _paged

@@ -1,7 +1,8 @@
-"""Builds libbinattn.so (the C-ABI library, for sm_100a with nvcc) and _paged.so (a Python module) in-tree."""
+"""Builds libbinattn.so (the C-ABI library, for sm_100a with nvcc) and _paged (a Python module) in-tree."""
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import os
 import subprocess
 import sys
@@ -14,7 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbinattn.so")
-MODULE = os.path.join(PKG, "_paged.so")
+MODULE = os.path.join(PKG, "_paged" + sysconfig.get_config_var("EXT_SUFFIX"))  # of this Python
+STAMP = os.path.join(BUILD, "paged_built_for")
 MODULE_SRC = os.path.join(CSRC, "paged_binding.cpp")
 NVCC = os.environ.get("NVCC", "nvcc")
 CXX = os.environ.get("CXX", "g++")
@@ -38,27 +40,48 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def installed_torch() -> str:
+    """What the Python module is compiled against: it takes tensors apart as this torch lays them out. (Found without
+    importing it.)"""
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return "unknown"
+
+
+def module_up_to_date() -> bool:
+    try:
+        with open(STAMP) as f:
+            same = f.read() == installed_torch()
+    except OSError:
+        return False
+    deps = [MODULE_SRC, os.path.join(INCLUDE, "binattn.h")]
+    return same and os.path.exists(MODULE) and all(os.path.getmtime(f) <= os.path.getmtime(MODULE) for f in deps)
+
+
 def build_module(force: bool = False) -> str | None:
-    """The Python module of the paged cache's entry points, against this interpreter's torch; None where there is no
-    torch (the C library needs none)."""
+    """The Python module of the paged cache's entry points, for this interpreter and its torch; None where there is
+    no torch (the C library needs none)."""
+    if not force and module_up_to_date():
+        return MODULE
     try:
         import torch
     except ImportError as e:
         print(f"no Python module of the paged cache's calls: {e}", file=sys.stderr)
         return None
-    deps = [MODULE_SRC, os.path.join(INCLUDE, "binattn.h")]
-    if not force and os.path.exists(MODULE) and all(os.path.getmtime(f) <= os.path.getmtime(MODULE) for f in deps):
-        return MODULE
+    os.makedirs(BUILD, exist_ok=True)
     home = os.path.dirname(os.path.abspath(torch.__file__))
     tmp = MODULE + f".tmp{os.getpid()}"
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
            "-I", os.path.join(home, "include"), "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", MODULE_SRC, "-o", tmp,
-           "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DBA_BUILT_FOR="torch {torch.__version__}"',
+           MODULE_SRC, "-o", tmp, "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{CXX} failed for {MODULE_SRC}:\n{r.stderr}")
     os.replace(tmp, MODULE)
+    with open(STAMP, "w") as f:
+        f.write(installed_torch())
     return MODULE
 
 

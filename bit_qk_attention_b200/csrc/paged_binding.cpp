@@ -277,4 +277,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged", nullptr, -1, methods, nul
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__paged() { return PyModule_Create(&module); }
+// built_for: the torch whose tensors this module can take.
+PyMODINIT_FUNC PyInit__paged() {
+  PyObject* m = PyModule_Create(&module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "built_for", BA_BUILT_FOR) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -56,3 +56,41 @@ def test_with_torch_both_are_built_once(tree):
     assert sum(".cpp" in c for c in done) == 1 and any(".cu.o" in c for c in done)
     assert [f for f in os.listdir(tree.path) if f.startswith("_paged")]
     assert tree(BUILD) == []
+
+
+OTHER_TORCH = """
+import importlib.metadata
+real = importlib.metadata.version
+importlib.metadata.version = lambda name: "9.9.9" if name == "torch" else real(name)
+"""
+
+
+def test_the_module_is_built_again_for_another_torch(tree):
+    tree(BUILD)
+    done = tree(OTHER_TORCH + BUILD)
+    assert len(done) == 1 and ".cpp" in done[0] and 'BA_BUILT_FOR="torch ' in done[0]
+    assert tree(OTHER_TORCH + BUILD) == []
+    assert len(tree(BUILD)) == 1
+
+
+def test_the_module_is_named_for_its_python(tree):
+    import sysconfig
+    tree(BUILD)
+    assert [f for f in os.listdir(tree.path) if f.startswith("_paged")] == ["_paged" + sysconfig.get_config_var("EXT_SUFFIX")]
+
+
+@pytest.mark.parametrize("module", ["built_for = 'torch 1.2.3'", "", None])
+def test_a_module_of_another_torch_is_not_called(tree, module):
+    """A module for another torch, one from before it said so, and none at all: the message says what to do."""
+    if module is not None:
+        (tree.path / "_paged.py").write_text(module + "\ndef bind(*a):\n    raise SystemExit('called')\n")
+    tree("""
+        import bit_qk_attention_b200 as ba
+        ba.lib = lambda: None
+        try:
+            ba._native()
+        except RuntimeError as e:
+            assert "build it with" in str(e), e
+        else:
+            raise SystemExit("not refused")
+        """)
