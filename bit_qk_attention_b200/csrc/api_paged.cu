@@ -124,8 +124,8 @@ ba_status plan(const ba_kv_cache* cache, const ba_paged_seqs* s, PagedAttnParams
   p->by_page = FastDiv::of(p->cache.page_size);
   p->by_tiles = FastDiv::of(p->row_tiles);
   const int64_t all = tiles * p->B * p->cache.heads;
-  // Row slots count in 31 bits, and so does a CTA's share of the key blocks (64 or 128 keys).
-  if (all > kMaxCtas / p->row_tile || all > (int64_t{1} << 38) / (p->max_kv_len / 64 + 16)) return BA_ERR_UNSUPPORTED;
+  // A CTA's share of the key blocks (64 or 128 keys) counts in 31 bits.
+  if (all > (int64_t{1} << 38) / (p->max_kv_len / 64 + 16)) return BA_ERR_UNSUPPORTED;
   if (p->row_tile == kChunkRows)
     paged_chunk_plan(p, sm_count());
   else

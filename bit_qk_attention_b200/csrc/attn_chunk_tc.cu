@@ -116,7 +116,7 @@ struct Walk {
       w = entry_tile(p, line.entry, kBlk);
       const int units = units_of(w, kCost);
       if (units == 0) {  // a tile without rows
-        ++line.entry;
+        line.entry = entry_after(p, line.entry, w);
         continue;
       }
       entry = line.entry;

@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CPG, NR))
   if (p.ctas > 0) {
     const int units = units_of(w, kCost);
     if (units == 0) {  // a tile without rows
-      ++line.entry;
+      line.entry = entry_after(p, line.entry, w);
       continue;
     }
     const int entry = line.entry;

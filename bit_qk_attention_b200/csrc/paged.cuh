@@ -160,6 +160,12 @@ __device__ __forceinline__ RowTile entry_tile(const PagedAttnParams& p, int entr
 
 __device__ __forceinline__ int units_of(const RowTile& w, int cost) { return w.rows > 0 ? cost + w.nblk : 0; }
 
+// The entry after one: the next tile, or, behind a sequence's last row, where there may be any number of tiles
+// without rows (as many as max_q_len has), the next sequence.
+__device__ __forceinline__ int entry_after(const PagedAttnParams& p, int entry, const RowTile& w) {
+  return w.rows > 0 ? entry + 1 : (p.by_tiles(entry) + 1) * p.row_tiles;
+}
+
 // A CTA's stretch [at, end) of the line, `per` units or fewer; `at` lies in `entry`, whose units
 // start at `base`.
 struct Stretch {
@@ -173,11 +179,17 @@ __device__ __forceinline__ Stretch find_stretch(const PagedAttnParams& p, int bk
   int64_t* s_warp = scratch;
   int64_t& s_base = scratch[THREADS / 32];
   int64_t& s_entry = scratch[THREADS / 32 + 1];
-  const int heads = p.cache.heads, n = p.B * p.row_tiles, each = (n + THREADS - 1) / THREADS;
-  const int i0 = min(n, static_cast<int>(threadIdx.x) * each), i1 = min(n, i0 + each);
+  // n < 2^31, but rounded up to a multiple of THREADS it may not be.
+  const int heads = p.cache.heads, n = p.B * p.row_tiles;
+  const unsigned end = n, each = (end + THREADS - 1) / THREADS;
+  const int i0 = min(end, threadIdx.x * each), i1 = min(end, (threadIdx.x + 1) * each);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int64_t sum = 0;
-  for (int i = i0; i < i1; ++i) sum += units_of(entry_tile(p, i, bk), cost);
+  for (int i = i0; i < i1;) {
+    const RowTile w = entry_tile(p, i, bk);
+    sum += units_of(w, cost);
+    i = entry_after(p, i, w);
+  }
   int64_t upto = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -202,10 +214,12 @@ __device__ __forceinline__ Stretch find_stretch(const PagedAttnParams& p, int bk
   int64_t base = before * heads;
   if (st.at < st.end && base <= st.at && st.at < base + sum * heads) {
     int i = i0;
-    for (;; ++i) {
-      const int64_t u = static_cast<int64_t>(units_of(entry_tile(p, i, bk), cost)) * heads;
+    while (true) {
+      const RowTile w = entry_tile(p, i, bk);
+      const int64_t u = static_cast<int64_t>(units_of(w, cost)) * heads;
       if (st.at < base + u) break;
       base += u;
+      i = entry_after(p, i, w);
     }
     s_entry = i;
     s_base = base;

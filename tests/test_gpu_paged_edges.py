@@ -94,3 +94,27 @@ def test_many_small_weights_beside_one_large(ba, large_scale, qn, below):
     want = below * math.log(2.0) + math.log1p(mass)
     assert ((lse.double() - want).abs() <= 2.0 ** -19 * 27 + n * 2.0 ** -26).all()
 
+
+# ----------------------------------------------------------------------------- sizes
+@pytest.mark.parametrize("bound", [None, 128])
+def test_a_large_batch_of_short_sequences_with_the_default_bound(ba, bound):
+    """65536 new tokens of 512 sequences in one call: the bound of their lengths is the number of all new tokens
+    unless the caller gives one."""
+    B, each, Hq, Hkv, d, ps = 512, 128, 64, 8, 16, 128
+    g = _gen(40)
+    c = ba.KVCache.zeros(B, Hkv, d, ps)
+    k, v = (torch.randn((B * each, Hkv, d), generator=g).bfloat16() for _ in range(2))
+    ba.cache_write(c, k.cuda(), v.cuda(), torch.arange(B * each).cuda())
+    q = torch.randn((B * each, Hq, d), generator=g).bfloat16()
+    kv = torch.full((B,), each, dtype=torch.int32)
+    kv[3], kv[200] = 60, 0  # fewer keys than new tokens
+    table = torch.arange(B, dtype=torch.int32)[:, None].contiguous()
+    cu = torch.arange(0, B * each + 1, each, dtype=torch.int32)
+    o, lse = _run(ba, (c, q, table, kv, cu), max_q_len=bound)
+    for b in (0, 3, 200, 511):
+        rows = slice(b * each, (b + 1) * each)
+        one = ba.KVCache(c.data[b:b + 1], ps, d)
+        ref = _ref(ba, (one, q[rows, ::8], torch.zeros((1, 1), dtype=torch.int32), kv[b:b + 1], torch.tensor([0, each])))
+        _compare(o[rows, ::8], lse[rows, ::8], ref, f"sequence {b}")
+    assert torch.isfinite(o).all()
+
