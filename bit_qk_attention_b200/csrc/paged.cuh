@@ -166,6 +166,13 @@ __device__ __forceinline__ int entry_after(const PagedAttnParams& p, int entry, 
   return w.rows > 0 ? entry + 1 : (p.by_tiles(entry) + 1) * p.row_tiles;
 }
 
+// Units of the line per CTA, rounded up: below 2^31 (the plan sees to it). In 32 bits where the sum fits, since
+// every CTA waits for this division.
+__host__ __device__ __forceinline__ int share_of(int64_t total, uint32_t ctas) {
+  const int64_t up = total + ctas - 1;
+  return static_cast<int>((up >> 32) == 0 ? static_cast<uint32_t>(up) / ctas : up / ctas);
+}
+
 // A CTA's stretch [at, end) of the line, `per` units or fewer; `at` lies in `entry`, whose units
 // start at `base`.
 struct Stretch {
@@ -206,9 +213,7 @@ __device__ __forceinline__ Stretch find_stretch(const PagedAttnParams& p, int bk
   }
   total *= heads;
   Stretch st;
-  st.per = max(min_units, static_cast<int>((total >> 32) == 0
-                                               ? (static_cast<uint32_t>(total) + gridDim.x - 1) / gridDim.x
-                                               : ceil_div(total, gridDim.x)));
+  st.per = max(min_units, share_of(total, gridDim.x));
   st.at = static_cast<int64_t>(blockIdx.x) * st.per;
   st.end = min(total, st.at + st.per);
   int64_t base = before * heads;
