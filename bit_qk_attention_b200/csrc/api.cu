@@ -484,14 +484,10 @@ int ba_get_attention_impl(void) { return g_impl.load(); }
 int ba_last_attention_impl(void) { return tl_last_impl; }
 
 ba_status ba_check_device_status(void* stream) {
+  const StatusWord words[] = {attention_status(), chunk_status(), decode_status()};
   bool expired = false;
-  for (auto read : {read_and_clear_device_status, read_and_clear_chunk_status, read_and_clear_decode_status}) {
-    int v = 0;
-    const ba_status st = cuda_status(read(&v, static_cast<cudaStream_t>(stream)));
-    if (st != BA_OK) return st;
-    expired |= v != 0;
-  }
-  return expired ? BA_ERR_TIMEOUT : BA_OK;
+  const ba_status st = cuda_status(collect_status(words, 3, static_cast<cudaStream_t>(stream), &expired));
+  return st != BA_OK ? st : (expired ? BA_ERR_TIMEOUT : BA_OK);
 }
 
 const char* ba_status_string(ba_status s) {

@@ -768,8 +768,8 @@ void paged_chunk_plan(PagedAttnParams* p, int sms) {
   p->ctas = p->whole ? static_cast<int>(tiles) : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, (blocks + kCost) * tiles / kMinUnits)));
 }
 
-cudaError_t read_and_clear_chunk_status(int* value, cudaStream_t s) {
-  return read_and_clear_status(g_chunk_status, value, s);
-}
+static cudaError_t read_chunk_status(int* value, cudaStream_t s) { return read_word(g_chunk_status, value, s); }
+static cudaError_t clear_chunk_status(cudaStream_t s) { return clear_word(g_chunk_status, s); }
+StatusWord chunk_status() { return {read_chunk_status, clear_chunk_status}; }
 
 }  // namespace binattn

@@ -801,8 +801,8 @@ void paged_decode_plan(PagedAttnParams* p, int sms) {
     p->ctas = static_cast<int>(std::min<int64_t>(fit, ceil_div((blocks + kCost) * tiles, kWarps)));
 }
 
-cudaError_t read_and_clear_decode_status(int* value, cudaStream_t s) {
-  return read_and_clear_status(g_decode_status, value, s);
-}
+static cudaError_t read_decode_status(int* value, cudaStream_t s) { return read_word(g_decode_status, value, s); }
+static cudaError_t clear_decode_status(cudaStream_t s) { return clear_word(g_decode_status, s); }
+StatusWord decode_status() { return {read_decode_status, clear_decode_status}; }
 
 }  // namespace binattn

@@ -1399,14 +1399,8 @@ cudaError_t launch_attn_tc(const AttnParams& p, cudaStream_t s) {
   }
 }
 
-cudaError_t read_and_clear_device_status(int* value, cudaStream_t s) {
-  cudaError_t e = cudaMemcpyFromSymbolAsync(value, g_device_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
-  if (e != cudaSuccess) return e;
-  if ((e = cudaStreamSynchronize(s)) != cudaSuccess) return e;
-  const int zero = 0;
-  if ((e = cudaMemcpyToSymbolAsync(g_device_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s)) != cudaSuccess)
-    return e;
-  return cudaStreamSynchronize(s);
-}
+static cudaError_t read_attention_status(int* value, cudaStream_t s) { return read_word(g_device_status, value, s); }
+static cudaError_t clear_attention_status(cudaStream_t s) { return clear_word(g_device_status, s); }
+StatusWord attention_status() { return {read_attention_status, clear_attention_status}; }
 
 }  // namespace binattn

@@ -89,10 +89,30 @@ cudaError_t launch_attn_tc(const AttnParams& p, cudaStream_t s);
 // BA_OK, or BA_ERR_CUDA with e kept for ba_last_cuda_error() on this thread.
 ba_status report_cuda(cudaError_t e);
 
-// Device status words of the kernels with bounded waits.
-cudaError_t read_and_clear_device_status(int* value, cudaStream_t s);
-cudaError_t read_and_clear_chunk_status(int* value, cudaStream_t s);
-cudaError_t read_and_clear_decode_status(int* value, cudaStream_t s);
+// Device status word of the kernels of one file: set when a bounded wait expires. Both calls wait for the stream.
+struct StatusWord {
+  cudaError_t (*read)(int* value, cudaStream_t s);
+  cudaError_t (*clear)(cudaStream_t s);
+};
+StatusWord attention_status();
+StatusWord chunk_status();
+StatusWord decode_status();
+
+// Reads all words before it clears any: an error leaves them as they are, for the next call. Only a word that
+// was set is cleared, and one that could not be stays to be reported again.
+inline cudaError_t collect_status(const StatusWord* words, int n, cudaStream_t s, bool* expired) {
+  uint32_t set = 0;
+  for (int i = 0; i < n; ++i) {
+    int value = 0;
+    const cudaError_t e = words[i].read(&value, s);
+    if (e != cudaSuccess) return e;
+    if (value != 0) set |= 1u << i;
+  }
+  *expired = set != 0;
+  for (int i = 0; i < n; ++i)
+    if ((set >> i) & 1u) words[i].clear(s);
+  return cudaSuccess;
+}
 
 // Allows a kernel its dynamic shared memory, once per device.
 template <auto Kernel>
@@ -108,13 +128,16 @@ cudaError_t allow_smem(int bytes) {
 }
 
 template <typename Symbol>
-cudaError_t read_and_clear_status(Symbol& symbol, int* value, cudaStream_t s) {
-  cudaError_t e = cudaMemcpyFromSymbolAsync(value, symbol, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
-  if (e != cudaSuccess) return e;
-  if ((e = cudaStreamSynchronize(s)) != cudaSuccess) return e;
+cudaError_t read_word(Symbol& symbol, int* value, cudaStream_t s) {
+  const cudaError_t e = cudaMemcpyFromSymbolAsync(value, symbol, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  return e != cudaSuccess ? e : cudaStreamSynchronize(s);
+}
+
+template <typename Symbol>
+cudaError_t clear_word(Symbol& symbol, cudaStream_t s) {
   const int zero = 0;
-  if ((e = cudaMemcpyToSymbolAsync(symbol, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s)) != cudaSuccess) return e;
-  return cudaStreamSynchronize(s);
+  const cudaError_t e = cudaMemcpyToSymbolAsync(symbol, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+  return e != cudaSuccess ? e : cudaStreamSynchronize(s);
 }
 
 }  // namespace binattn

@@ -329,8 +329,8 @@ int ba_get_attention_impl(void);
 int ba_last_attention_impl(void);
 
 /*
- * Synchronises `stream` and reads (then clears) the device status word that kernels set
- * when a bounded wait expires. Returns BA_OK or BA_ERR_TIMEOUT (or BA_ERR_CUDA).
+ * Synchronises `stream` and reads (then clears) the device status words that kernels set
+ * when a bounded wait expires. Returns BA_OK or BA_ERR_TIMEOUT (or BA_ERR_CUDA, with nothing cleared).
  */
 ba_status ba_check_device_status(void* stream);
 
