@@ -425,7 +425,8 @@ def _native():
             raise RuntimeError(f"the module _paged has been built for {built_for}, and this is torch {torch.__version__}: "
                                "build it with `python -m bit_qk_attention_b200.build`")
         _paged.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
-            "ba_kv_block_bytes", "ba_cache_write", "ba_cache_read", "ba_paged_workspace_bytes", "ba_attention_paged")))
+            "ba_kv_block_bytes", "ba_cache_write", "ba_cache_read", "ba_paged_workspace_bytes", "ba_attention_paged")),
+            torch.OutOfMemoryError)
         _module = _paged
     return _module
 

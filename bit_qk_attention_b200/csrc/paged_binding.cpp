@@ -25,6 +25,8 @@ decltype(&ba_cache_read) f_read = nullptr;
 decltype(&ba_paged_workspace_bytes) f_workspace = nullptr;
 decltype(&ba_attention_paged) f_attend = nullptr;
 
+PyObject* out_of_memory = nullptr;  // torch.OutOfMemoryError
+
 struct Refused : std::runtime_error {
   PyObject* type;
   Refused(PyObject* t, const std::string& what) : std::runtime_error(what), type(t) {}
@@ -115,21 +117,25 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t wanted, F&& f) {
     return f();
   } catch (const Refused& e) {
     if (e.type != nullptr) PyErr_SetString(e.type, e.what());
+  } catch (const c10::OutOfMemoryError& e) {
+    PyErr_SetString(out_of_memory, e.what_without_backtrace());
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   }
   return nullptr;
 }
 
-// bind(addresses of the five C functions)
+// bind(addresses of the five C functions, torch.OutOfMemoryError)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return guarded(n, 5, [&]() -> PyObject* {
+  return guarded(n, 6, [&]() -> PyObject* {
     auto at_ = [&](int i) { return reinterpret_cast<void*>(static_cast<intptr_t>(whole(args[i]))); };
     f_block_bytes = reinterpret_cast<decltype(f_block_bytes)>(at_(0));
     f_write = reinterpret_cast<decltype(f_write)>(at_(1));
     f_read = reinterpret_cast<decltype(f_read)>(at_(2));
     f_workspace = reinterpret_cast<decltype(f_workspace)>(at_(3));
     f_attend = reinterpret_cast<decltype(f_attend)>(at_(4));
+    Py_INCREF(args[5]);
+    out_of_memory = args[5];
     Py_RETURN_NONE;
   });
 }

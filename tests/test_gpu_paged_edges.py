@@ -118,3 +118,22 @@ def test_a_large_batch_of_short_sequences_with_the_default_bound(ba, bound):
         _compare(o[rows, ::8], lse[rows, ::8], ref, f"sequence {b}")
     assert torch.isfinite(o).all()
 
+
+# ----------------------------------------------------------------------------- errors
+def test_an_allocation_that_fails_raises_out_of_memory(ba):
+    """Results that do not fit the device: the error that a server catches, and the next call works."""
+    c = ba.KVCache.zeros(1, 1, 128, 16)
+    T, H = 4_000_000, 128  # 262 GB of fp32 results; q and the lists take next to nothing
+    q = torch.zeros((1, 1, 128), dtype=torch.bfloat16, device="cuda").expand(T, H, 128)
+    table, kv = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    with pytest.raises(torch.OutOfMemoryError):
+        ba.attention_paged(q, c, table, kv, cu, max_q_len=1, out_dtype=torch.float32)
+    slots = torch.zeros(1, dtype=torch.int64, device="cuda").expand(T * H // 16).contiguous()
+    big = ba.KVCache(c.data.expand(1, 16, -1).contiguous(), 16, 128)
+    with pytest.raises(torch.OutOfMemoryError):
+        ba.cache_read(big, slots, torch.float32)
+    o = ba.attention_paged(q[:1], c, table, kv, cu, max_q_len=1)
+    torch.cuda.synchronize()
+    assert not o[0].any()
+
