@@ -486,7 +486,7 @@ def attention_paged(q, cache: KVCache, page_table, kv_lens, cu_seqlens_q=None, m
     max_q_len, max_kv_len: host bounds of the lengths (defaults: T, and the page table's tokens).
                   Tight bounds let the launch be chosen well; lengths are read on the device.
     window:       > 0: a token sees itself and the window - 1 tokens before it, and the first `sinks`.
-    workspace:    uint8 CUDA tensor of at least the bytes that ba_paged_workspace_bytes tells
+    workspace:    uint8 CUDA tensor of at least the bytes that paged_workspace_bytes tells for the same arguments
                   (default: allocated for the call). Calls that can overlap need one each.
     Returns o [T, n_heads, d] (out_dtype, default q's; rows of no sequence are left as they were in
     `out`), and with return_lse also the fp32 log of the softmax sums [T, n_heads].
@@ -504,6 +504,26 @@ def attention_paged(q, cache: KVCache, page_table, kv_lens, cu_seqlens_q=None, m
     if r.__class__ is int:
         _check(r, "ba_attention_paged")
     return r
+
+
+def paged_workspace_bytes(q, cache: KVCache, page_table, kv_lens, cu_seqlens_q=None, max_q_len: Optional[int] = None,
+                          max_kv_len: Optional[int] = None, causal: bool = True, window: int = 0, sinks: int = 0) -> int:
+    """Bytes of workspace that attention_paged needs for these arguments (ba_paged_workspace_bytes; 0: none). Only
+    the tensors' shapes and the bounds count, so that one workspace does for every call with the same ones."""
+    T, n_heads, _ = q.shape
+    most = 0x7fffffff  # what a C int holds: larger bounds mean the same
+    pages = page_table.shape[1]
+    if max_q_len is None:
+        max_q_len = T if cu_seqlens_q is not None else 1
+    keys = pages * cache.page_size
+    cu = None if cu_seqlens_q is None else cu_seqlens_q.data_ptr()
+    seqs = CPagedSeqs(kv_lens.numel(), T, n_heads, min(max_q_len, most), keys if max_kv_len is None else min(max_kv_len, keys),
+                      cu, kv_lens.data_ptr(), page_table.data_ptr(), page_table.stride(0), pages, int(causal),
+                      min(window, most), min(sinks, most))
+    need = lib().ba_paged_workspace_bytes(ctypes.byref(cache.c()), ctypes.byref(seqs))
+    if need == ctypes.c_size_t(-1).value:
+        raise ValueError("sizes or bounds that attention_paged refuses")
+    return need
 
 
 def bias_from_workload(w, device) -> Optional[Bias]:

@@ -137,3 +137,26 @@ def test_an_allocation_that_fails_raises_out_of_memory(ba):
     torch.cuda.synchronize()
     assert not o[0].any()
 
+
+@pytest.mark.parametrize("qn,kn,kw", [([1], [20000], {}), ([1, 1], [9000, 40], dict(max_q_len=1)), ([60, 200], [9000, 4000], {}),
+                                      ([60, 200], [9000, 4000], dict(max_q_len=200, max_kv_len=1 << 40, window=1 << 35, sinks=3)),
+                                      ([3], [40], {})])
+def test_a_workspace_of_the_bytes_that_the_package_tells(ba, qn, kn, kw):
+    """With the bytes of paged_workspace_bytes the call gives what it gives by itself; with 16 fewer it is refused."""
+    c, q, table, kv, cu = _problem(ba, qn, kn, 8, 2, 128, 64, "bf16", 50)
+    args = (q.cuda(), c, table.cuda(), kv.cuda(), cu.cuda())
+    need = ba.paged_workspace_bytes(*args, **kw)
+    want = ba.attention_paged(*args, **kw)
+    guard = torch.full((need + 256,), 0xAB, dtype=torch.uint8, device="cuda")
+    got = ba.attention_paged(*args, workspace=guard[:need], **kw)
+    assert torch.equal(got, want) and (guard[need:] == 0xAB).all()
+    if need:
+        with pytest.raises(ba.BinAttnError) as e:
+            ba.attention_paged(*args, workspace=guard[:need - 16], **kw)
+        assert e.value.status == 4
+    else:
+        assert kn == [40]
+    with pytest.raises(ValueError):
+        ba.paged_workspace_bytes(*args, window=-1)
+    torch.cuda.synchronize()
+
