@@ -216,13 +216,13 @@ __global__ void __launch_bounds__(256) paged_q_kernel(PagedAttnParams p, uint4* 
   for (int k = 0; k < 4; ++k) {
     const float x = 32 * k + lane < p.cache.d ? load1<T>(src + 32 * k + lane) : 0.0f;
     word[k] = __ballot_sync(0xffffffffu, x < 0.0f);
-    sum += fabsf(x);
+    sum += fabsf(x) * kMeanStep;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) {
     bits[row] = make_uint4(word[0], word[1], word[2], word[3]);
-    mu[row] = sum / static_cast<float>(p.cache.d);
+    mu[row] = mean_of(sum, p.cache.d);
   }
 }
 

@@ -337,13 +337,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CPG, NR))
     for (int k = 0; k < 4; ++k) {
       const float x = widen(q_raw[u][k], q_f16);
       word[k] = __ballot_sync(0xffffffffu, x < 0.0f);
-      sum += fabsf(x);
+      sum += fabsf(x) * kMeanStep;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const int r = warp + u * kWarps;
     if (lane < 4) s_bits[r][lane] = lane == 0 ? word[0] : (lane == 1 ? word[1] : (lane == 2 ? word[2] : word[3]));
-    if (lane == 0) s_mu[r] = sum / static_cast<float>(cv.d);
+    if (lane == 0) s_mu[r] = mean_of(sum, cv.d);
   }
   __syncthreads();
 

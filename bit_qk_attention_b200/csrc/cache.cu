@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheWriteParams 
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     neg |= (k[i] < 0.0f ? 1u : 0u) << i;
-    sum += fabsf(k[i]);
+    sum += fabsf(k[i]) * kMeanStep;
     amax = fmaxf(amax, fabsf(v[i]));
   }
 #pragma unroll
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheWriteParams 
   blk[cv.off_bits() + off * 16 + c0 / 8] = static_cast<uint8_t>(neg);
   const int e = row_exp(amax);
   if (c0 == 0) {
-    *reinterpret_cast<__nv_bfloat16*>(blk + cv.off_mu() + off * 2) = __float2bfloat16_rn(sum / static_cast<float>(cv.d));
+    *reinterpret_cast<__nv_bfloat16*>(blk + cv.off_mu() + off * 2) = __float2bfloat16_rn(mean_of(sum, cv.d));
     *reinterpret_cast<int8_t*>(blk + cv.off_exp() + off) = static_cast<int8_t>(e);
   }
   if (c0 < cv.dp) {

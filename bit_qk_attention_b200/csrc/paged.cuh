@@ -252,6 +252,11 @@ __device__ __forceinline__ PageAt page_at(const PagedAttnParams& p, const int32_
   return at;
 }
 
+// The mean of d numbers |x| is the sum of |x| * kMeanStep over d * kMeanStep: exact steps of a power of two that
+// keep 128 of the largest bf16 numbers within fp32's range (and the least ones above its end).
+constexpr float kMeanStep = 0.0078125f;
+__device__ __forceinline__ float mean_of(float sum, int d) { return sum / (static_cast<float>(d) * kMeanStep); }
+
 // A 16-bit number, widened.
 __device__ __forceinline__ float widen(uint16_t x, int f16) {
   return f16 ? __half2float(__ushort_as_half(x)) : __uint_as_float(static_cast<uint32_t>(x) << 16);

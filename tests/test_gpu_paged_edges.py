@@ -160,3 +160,37 @@ def test_a_workspace_of_the_bytes_that_the_package_tells(ba, qn, kn, kw):
         ba.paged_workspace_bytes(*args, window=-1)
     torch.cuda.synchronize()
 
+
+# ----------------------------------------------------------------------------- ends of bf16's range
+@pytest.mark.parametrize("d", [1, 5, 32, 72, 128])
+def test_write_of_the_largest_numbers(ba, d):
+    """The mean of numbers near bf16's largest is one of them, though their sum is beyond fp32; and the mean of the
+    least ones does not vanish."""
+    ps, top, least = 16, torch.finfo(torch.bfloat16).max, 2.0 ** -133
+    g = _gen(d)
+    rows = [torch.full((d,), top), -torch.full((d,), top), torch.full((d,), top / 2), torch.full((d,), least),
+            torch.full((d,), 3 * least), torch.rand((d,), generator=g) * top,
+            torch.full((d,), torch.finfo(torch.bfloat16).smallest_normal)]
+    k = torch.stack(rows).bfloat16()[:, None]
+    v = torch.randn(k.shape, generator=g).bfloat16()
+    c = ba.KVCache.zeros(1, 1, d, ps)
+    slots = torch.arange(len(rows))
+    ba.cache_write(c, k.cuda(), v.cuda(), slots.cuda())
+    _check_rows(c.data.cpu(), ps, d, k, v, slots)
+    kk, _ = ba.cache_read(c, slots.cuda(), torch.float32)
+    assert torch.isfinite(kk).all()
+
+
+@pytest.mark.parametrize("qn", [1, 20, 150])
+def test_queries_of_the_largest_numbers(ba, qn):
+    """mean |q| within fp32 although the sum is not; keys as small make scores of ordinary size."""
+    d, ps, n = 64, 16, 300
+    g = _gen(qn)
+    c = ba.KVCache.zeros(-(-n // ps), 1, d, ps)
+    k, v = (torch.randn((n, 1, d), generator=g) for _ in range(2))
+    ba.cache_write(c, (k * 2.0 ** -122).bfloat16().cuda(), v.bfloat16().cuda(), torch.arange(n).cuda())
+    q = (torch.randn((qn, 2, d), generator=g).sign() * 2.0 ** 123).bfloat16()
+    prob = (c, q, torch.arange(c.num_pages, dtype=torch.int32)[None], torch.tensor([n], dtype=torch.int32),
+            torch.tensor([0, qn], dtype=torch.int32))
+    _compare(*_run(ba, prob), _ref(ba, prob))
+
