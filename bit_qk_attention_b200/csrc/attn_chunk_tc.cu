@@ -68,6 +68,9 @@ constexpr float kBelow = 7.0f, kLeastBelow = 3.0f;
 constexpr float kHigh = 9.9f;
 constexpr float kMostLog2 = 15.9f;    // log2 of weights that fp16 surely holds
 constexpr float kMostSum = 65504.0f;  // fp16's largest number: a sum of weights up to this has none above it
+// A row's factor of its scores is this at least, also for a row of zeros, so that -inf in masked places stays -inf:
+// fp32's least number, which makes nothing of any finite score.
+constexpr float kLeastFactor = 1.4e-45f;
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 
 template <int CH>  // channels of the operands: 64 or 128 (>= d)
@@ -476,12 +479,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[bQfull + q]);
-      // Above 0 also for a row of zeros, so that -inf in masked places stays -inf.
-      return fmaxf(p.scale_log2 * mu, 1e-30f);
+      return fmaxf(p.scale_log2 * mu, kLeastFactor);
     };
     grid_dependency_wait();  // for the rows of q
     bool ok = true, more = k.next(p);
-    float cq_next = 1e-30f;
+    float cq_next = kLeastFactor;
     if (!more && threadIdx.x == 8 * 32 && !p.whole) p.notes[blockIdx.x].last = -1;  // nothing but the start of a cut one
     if (more && q < k.tiles() && k.n_blk > 0) cq_next = write_q(k);
     while (ok && more) {

@@ -194,3 +194,19 @@ def test_queries_of_the_largest_numbers(ba, qn):
             torch.tensor([0, qn], dtype=torch.int32))
     _compare(*_run(ba, prob), _ref(ba, prob))
 
+
+@pytest.mark.parametrize("qn", [1, 20, 150])
+def test_queries_of_zeros_over_very_large_keys(ba, qn):
+    """A row of q that is 0 has scores of 0, however large the keys' scales are."""
+    d, ps, n = 64, 16, 300
+    g = _gen(qn + 1)
+    c = ba.KVCache.zeros(-(-n // ps), 1, d, ps)
+    k, v = (torch.randn((n, 1, d), generator=g) for _ in range(2))
+    ba.cache_write(c, (k * 2.0 ** 115).bfloat16().cuda(), v.bfloat16().cuda(), torch.arange(n).cuda())
+    q = torch.zeros((qn, 2, d), dtype=torch.bfloat16)
+    q[::3, 1] = (torch.randn((d,), generator=g) * 2.0 ** -115).bfloat16()  # and one whose scores are ordinary
+    prob = (c, q, torch.arange(c.num_pages, dtype=torch.int32)[None], torch.tensor([n], dtype=torch.int32),
+            torch.tensor([0, qn], dtype=torch.int32))
+    for causal in (True, False):
+        _compare(*_run(ba, prob, causal=causal), _ref(ba, prob, causal=causal))
+
