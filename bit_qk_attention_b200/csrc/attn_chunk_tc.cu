@@ -432,7 +432,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
           if (32 * i < cv.d) expand_signs(kd + i * 4096, word[i], 0xffffffffu);
         fence_proxy_async_smem();
         __syncwarp();
+#ifdef BA_TEST_SKIP_ARRIVE
+        // Test build only: the first block's arrival is withheld, so that the waits behind it run into the limit.
+        if (lane == 0 && g != 0) mbar_arrive(&bars[bKfull + st]);
+#else
         if (lane == 0) mbar_arrive(&bars[bKfull + st]);
+#endif
         if (g >= 2 && !(ok = wait_warp<true>(&bars[bVempty + st], ((g >> 1) - 1) & 1, abort_flag))) break;
         const uint32_t vd = base + C::offV + st * C::kOp16 + row * 16;
         // A row that no query row sees may hold anything: times 0 it is finite, as its weight of 0 needs.

@@ -308,7 +308,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CPG, NR))
     // Bits 0, 4, 8 and 12 of the vote: the pieces with a page.
     const uint32_t vote = __ballot_sync(0xffffffffu, page >= 0 && lane < 16) & 0x1111u;
     const uint32_t bar = smem_u32(&s_full[warp][to]), extra = xring + to * S::kX + xdst;
-    if (lane == 0) mbar_arrive_expect_tx(&s_full[warp][to], __popc(vote) * unit * S::kToken);
+#ifdef BA_TEST_SKIP_ARRIVE
+    // Test build only: the first block waits for 16 bytes that nobody brings, so that its wait runs into the limit.
+    const uint32_t missing = n == 0 ? 16u : 0u;
+#else
+    constexpr uint32_t missing = 0u;
+#endif
+    if (lane == 0) mbar_arrive_expect_tx(&s_full[warp][to], __popc(vote) * unit * S::kToken + missing);
     __syncwarp();
     if (lane < 4 * per) {
       if (page < 0) {
