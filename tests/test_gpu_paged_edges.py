@@ -210,3 +210,58 @@ def test_queries_of_zeros_over_very_large_keys(ba, qn):
     for causal in (True, False):
         _compare(*_run(ba, prob, causal=causal), _ref(ba, prob, causal=causal))
 
+
+# ----------------------------------------------------------------------------- the roundings of each kernel
+def _weighed(prob, scale, few):
+    """(o, lse, tolerances) of a causal problem, with the roundings of one kernel and no others.
+
+    A score is a product of five fp32 numbers (mean |q| a sum of at most 9 steps and a quotient, the scale four
+    operations more): within 2^-24 (20 |s| + 40) of s + e ln 2, |e| <= 24. exp2 adds 2^-21 at most. Sums of m
+    positive numbers take m / 16 + 20 steps of 2^-24 at most. Numerator and softmax sum have both.
+    Few rows: a weight w 2^e is off by half of 1 / 65280 of the largest of its 64 keys. Many: by 2^-11 of itself, or
+    2^-28 of the row's largest. o rounds once to fp32."""
+    c, q, table, kv_lens, cu = prob
+    codes, _, neg, mu, ex = paged_ref.split_block(c.data.cpu(), c.page_size, c.d)
+    T, Hq, d = q.shape
+    G = Hq // c.n_kv_heads
+    o, lse = torch.zeros((T, Hq, d), dtype=F64), torch.zeros((T, Hq), dtype=F64)
+    to, tl = torch.zeros_like(o), torch.zeros_like(lse)
+    for b in range(len(kv_lens)):
+        n, t0, t1 = int(kv_lens[b]), int(cu[b]), int(cu[b + 1])
+        j = torch.arange(n)
+        pg, off = table[b].long()[j // c.page_size], j % c.page_size
+        for h in range(Hq):
+            k = torch.where(neg[pg, h // G, off][:, :d], -1.0, 1.0).to(F64) * mu[pg, h // G, off][:, None]
+            e = 2.0 ** ex[pg, h // G, off].to(F64)
+            code = codes[pg, h // G, off].to(F64)
+            for i in range(t1 - t0):
+                m = n - (t1 - t0) + i + 1
+                x = q[t0 + i, h].to(F64)
+                s = k[:m] @ (torch.where(x < 0, -1.0, 1.0).to(F64) * x.abs().mean() * scale)
+                w, big = torch.softmax(s, 0), float(s.abs().max())
+                we = w * e[:m]
+                out, A = we @ code[:m], we @ code[:m].abs()
+                rel = 2.0 ** -24 * (20 * big + 40) + 2.0 ** -21 + (m / 16 + 20) * 2.0 ** -24
+                if few:
+                    pad = (-m) % 64
+                    top = torch.nn.functional.pad(we, (0, pad)).view(-1, 64).amax(1)
+                    size = torch.nn.functional.pad(code[:m].abs(), (0, 0, 0, pad)).view(-1, 64, d).sum(1)
+                    off_by = 0.5 / 65280 * (1 + 2.0 ** -10) * (top @ size)
+                else:
+                    off_by = 2.0 ** -11 * A + 2.0 ** -28 * w.max() * (e[:m, None] * code[:m].abs()).sum(0)
+                o[t0 + i, h], lse[t0 + i, h] = out, torch.logsumexp(s, 0)
+                to[t0 + i, h] = off_by + 2 * rel * A + out.abs() * 2.0 ** -24
+                tl[t0 + i, h] = rel + lse[t0 + i, h].abs() * 2.0 ** -23
+    return o, lse, to, tl
+
+
+@pytest.mark.parametrize("d", [64, 72, 128])
+@pytest.mark.parametrize("qn,kn,few", [([1], [1000], True), ([1, 1, 1], [64, 700, 129], True), ([4], [333], True), ([9], [500], True),
+                                       ([70], [900], False), ([65, 90], [80, 400], False)])
+def test_weights_have_the_bits_that_are_documented(ba, qn, kn, few, d):
+    """fp32 results against the roundings of the kernel that makes them: some 2^-17 for few rows, 2^-11 for many."""
+    prob = _problem(ba, qn, kn, 4, 2, d, 32, "bf16", 70 + d)
+    scale = 0.25 / math.sqrt(d)
+    got = _run(ba, prob, dt_out=torch.float32, softmax_scale=scale, max_q_len=max(qn))
+    _compare(*got, _weighed(prob, scale, few))
+
