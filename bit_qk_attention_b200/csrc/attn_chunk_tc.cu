@@ -67,6 +67,7 @@ constexpr int kThreads = 512;  // service, expanding and two softmax warpgroups
 constexpr float kBelow = 7.0f, kLeastBelow = 3.0f;
 constexpr float kHigh = 9.9f;
 constexpr float kMostLog2 = 15.9f;    // log2 of weights that fp16 surely holds
+constexpr float kBoundUp = 1.000001f; // more than the roundings of a score and of its bound
 constexpr float kMostSum = 65504.0f;  // fp16's largest number: a sum of weights up to this has none above it
 // A row's factor of its scores is this at least, also for a row of zeros, so that -inf in masked places stays -inf:
 // fp32's least number, which makes nothing of any finite score.
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
       // A score passes M by more than the slack: M moves, and what there is of the row is rescaled. O
       // holds the halves before half h of block n.
       auto move_to = [&](float top, float bound, int n, int h) {
-        const bool moves = top > M + kHigh;
+        const bool moves = top - M > kHigh;
         // The bound may grow by 1 with the scales of the keys to come.
         const float to = fminf(top - kLeastBelow, fmaxf(top - kBelow, bound + (1.0f - kMostLog2)));
         const float f = moves ? ex2_approx(M - to) : 1.0f;  // 0 for a row's first keys
@@ -622,9 +623,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
             // among the half's scales, seen or not, fails the comparison.
             const volatile uint32_t* most = reinterpret_cast<volatile uint32_t*>(smem + C::offTop + (g & 3) * 16 + h * 8);
             const float mu_top = __uint_as_float(max(most[0], most[1]));
-            const float bound = cq * static_cast<float>(cv.d) * mu_top;
+            const float bound = cq * (static_cast<float>(cv.d) * kBoundUp) * mu_top;
             uint32_t z[16], y[8];
-            if (!__all_sync(0xffffffffu, !live || bound <= M + kMostLog2)) {
+            if (!__all_sync(0xffffffffu, !live || bound - M <= kMostLog2)) {
               float top = -CUDART_INF_F;
 #pragma unroll 1
               for (int k = 0; k < 4; ++k) {
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttnParam
                 for (int i = 0; i < 16; i += 2) top = fmax3(top, __uint_as_float(z[i]), __uint_as_float(z[i + 1]));
               }
               top *= cq;
-              if (__any_sync(0xffffffffu, top > M + kHigh)) {
+              if (__any_sync(0xffffffffu, top - M > kHigh)) {
                 move_to(top, bound, n, h);
                 if (!ok) break;
               }

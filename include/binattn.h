@@ -279,7 +279,8 @@ ba_status ba_cache_read(const ba_kv_cache* cache, const int64_t* slots, int64_t 
  * sums of 64 keys are added in fp32. Scores, maxima and sums are fp32. A row that sees nothing gets
  * o = 0 and lse = -inf.
  * Rows of the cache that no new token sees may hold anything. A row of o and lse is unspecified where
- * softmax_scale * mu_q * d or mu_j * d of a key that it sees is beyond fp32's range.
+ * softmax_scale * mu_q * d or mu_j * d of a key that it sees is beyond fp32's range, or a score s_j beyond
+ * +-2^24, where neighbouring fp32 numbers lie more than 1 apart.
  * BA_ERR_UNSUPPORTED where T * n_heads passes 2^31 - 4096, where the bounds make more than 2^31 - 1 tiles
  * (B * n_kv_heads * ceil(max_q_len * G / 256); 8 or 16 rows a tile with few), or where tiles * max_kv_len
  * passes some 2^44.

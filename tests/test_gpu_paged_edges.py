@@ -265,3 +265,33 @@ def test_weights_have_the_bits_that_are_documented(ba, qn, kn, few, d):
     got = _run(ba, prob, dt_out=torch.float32, softmax_scale=scale, max_q_len=max(qn))
     _compare(*got, _weighed(prob, scale, few))
 
+
+# ----------------------------------------------------------------------------- very large scores
+@pytest.mark.parametrize("scale", [1e3, 6e4])
+@pytest.mark.parametrize("qn", [1, 20, 150])
+def test_scores_up_to_the_limit(ba, qn, scale):
+    """Scores of up to 2^24: each row's largest key takes all, though neighbouring fp32 numbers lie 1 apart.
+
+    The keys' scales are 2^(-j / 8) in an order of its own, and all keys have the signs of q but for one channel, so
+    that the largest visible score is 2^(1/8) or more above the next. (A bf16 scale is off by 2^-8 of itself.) The weight of
+    that key, 1 or near it, may round to fp16."""
+    d, ps, n = 128, 16, 400
+    g = _gen(qn)
+    sign = torch.randn((d,), generator=g).sign()
+    k = sign * (2.0 ** (-torch.randperm(n, generator=g) / 8.0))[:, None]
+    k[:, 0] *= -1.0
+    v = torch.randn((n, 1, d), generator=g).bfloat16()
+    c = ba.KVCache.zeros(-(-n // ps), 1, d, ps)
+    ba.cache_write(c, k[:, None].bfloat16().cuda(), v.cuda(), torch.arange(n).cuda())
+    q = (sign * (1 + torch.rand((qn, 2, 1), generator=g))).bfloat16()
+    prob = (c, q, torch.arange(c.num_pages, dtype=torch.int32)[None], torch.tensor([n], dtype=torch.int32),
+            torch.tensor([0, qn], dtype=torch.int32))
+    mu, vh = c.k_mu[:, 0].flatten()[:n].float().cpu(), ba.cache_read(c, torch.arange(n).cuda(), torch.float32)[1][:, 0].cpu()
+    for causal in (True, False):
+        o, lse = _run(ba, prob, dt_out=torch.float32, softmax_scale=scale, causal=causal)
+        for i in range(qn):
+            top = int(mu[:n - qn + i + 1 if causal else n].argmax())
+            want = scale * q[i].double().abs().mean(-1) * float(mu[top]) * (d - 2)
+            assert ((o[i].cpu() - vh[top]).abs() <= vh[top].abs() * (2.0 ** -11 + 2.0 ** -20)).all(), (causal, i)
+            assert ((lse[i].cpu().double() - want).abs() <= want * 2.0 ** -20).all()
+
