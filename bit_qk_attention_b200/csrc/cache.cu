@@ -12,9 +12,10 @@
 // neighbour taking the next token of the same head.) Stores of read rows are streaming: they are as
 // large as all of L2 on long contexts.
 //
-// 16384 tokens x 8 heads x 128 channels (d): written in 20 us (4.3 TB/s; a third of the bytes are small
-// pieces of pages in any order), read in 14 us (6.2 TB/s, all from L2); 65536 tokens read in 72 to 78
-// us (4.4 to 4.8 TB/s); 8 tokens of 16 heads 1.8 us each way, of which a launch alone is most.
+// 16384 tokens x 8 heads x 128 channels (d): written in 20 us (4.3 TB/s of 512 bytes read and 147 written a row, 19 of
+// which in pieces of 16, 2 and 1; what binds it is not established), read in 14 us (6.2 TB/s, all from L2); 65536
+// tokens read in 72 to 78 us (4.4 to 4.8 TB/s, nor there); 8 tokens of 16 heads 1.8 us each way, of which a launch
+// alone is most.
 #include "kernels.h"
 #include "paged.cuh"
 
