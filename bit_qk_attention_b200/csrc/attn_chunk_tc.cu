@@ -55,7 +55,8 @@ using namespace ptx;
 constexpr int kBlk = 128;      // keys per block: N of QK, K of PV
 constexpr int kTile = 128;     // rows per tile: M
 // Blocks that a CTA could do while it starts and ends a (tile, head): with 1, 2, 4 and 6 a prompt of 2 x
-// 8192 tokens in a window took 235, 201, 199 and 200 us, chunks of 4 x 1000 over 9000 keys 192, 189, 180, 180.
+// 8192 tokens in a window took 235, 201, 199 and 200 us (with M at the largest score; see kBelow), chunks of 4 x 1000
+// over 9000 keys 192, 189, 180, 180.
 constexpr int kCost = 4;
 constexpr int kWholeBlocks = 10; // blocks that cutting a (tile, head) has to save
 constexpr int kMinUnits = 6;   // units (blocks, and kCost) a CTA takes at least

@@ -29,7 +29,7 @@
 //     joined through distributed shared memory. Else the CTAs share the line of all units evenly, and the
 //     parts of what they cut leave (M, sum, unnormalised o) in fp32, joined by a second kernel that is
 //     launched as a programmatic dependent.
-// Measured with 32 query heads, 8 KV heads, d = 128: 128 contexts up to 8192 tokens 104 to 107 us (5.6 to
+// Measured with 32 query heads, 8 KV heads, d = 128: 128 contexts up to 8192 tokens 105 to 107 us (5.6 to
 // 5.7 TB/s, 87 % of a copy; further keys come at 6.3 TB/s); one context of 1024 tokens 8 us, of which a few
 // dependent loads and cold instructions are most; 4 KV heads, one context of 131072 tokens 27 us (2.8
 // TB/s: 10 us are start and join). d = 64, one query head for each of 16 KV heads, a window of 4096 tokens
